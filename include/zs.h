@@ -364,6 +364,142 @@ int zs_pack_state_bf16mv(const float *master, const uint16_t *m_bf16, const uint
 int zs_unpack_state_bf16mv(const float *state, float *master, uint16_t *m_bf16, uint16_t *v_bf16,
                            int64_t n, void *stream);
 
+/*
+ * Global gradient norm and clipping.
+ *
+ * Training clips the gradient by its norm over all parameters of all ranks
+ * before the optimizer step: with S the sum of the squares of every element,
+ *
+ *   norm = sqrt(S),  d = norm + eps
+ *   coef = 1 where d <= max_norm, else max_norm / d
+ *
+ * and every gradient element is multiplied by coef.  The norm calls form S,
+ * norm and coef on the device in a record the caller owns; the clipped step
+ * and zs_tensors_clip read coef there, so nothing waits on the host.  A rank
+ * of several sums its own S into the others' (an all-reduce of the record's
+ * sumsq field, or an all-gather) and zs_clip_combine forms norm and coef of
+ * the total.
+ *
+ * Numerics: each element is squared and summed in binary64, where no square
+ * of an fp32 value overflows or vanishes; norm and coef are formed in binary64
+ * and rounded once to binary32.  The order of the sum is fixed by the sizes
+ * and the device, so the same call gives the same bits.
+ *
+ * Infinities and NaN: S is then infinite or NaN.  An infinite norm gives coef
+ * 0 (which turns infinite elements into NaN and the others into 0), a NaN norm
+ * coef NaN.  With rule->skip_nonfinite set, apply is 0 instead whenever the
+ * norm is not finite, and the clipped step and zs_tensors_clip then leave every
+ * buffer as it was: the step is skipped, as loss scaling wants it.
+ */
+typedef struct {
+    double sumsq;   /* S */
+    float norm;     /* sqrt(S) */
+    float coef;     /* what a clipped gradient is multiplied by, 0 .. 1 */
+    int32_t apply;  /* 0: a clipped step or zs_tensors_clip changes nothing; 1: it runs */
+    int32_t reserved;
+} zs_clip;          /* DEVICE record, 8-byte aligned */
+
+/* max_norm >= 0, may be infinite (coef is then 1); eps >= 0 and finite.  A
+ * null rule stands for an infinite max_norm and skip_nonfinite 0. */
+typedef struct {
+    float max_norm;
+    float eps;
+    int32_t skip_nonfinite;
+    int32_t reserved; /* must be 0 */
+} zs_clip_rule;
+
+/* Bytes of workspace a norm call needs: DEVICE memory of the caller, 8-byte
+ * aligned, contents irrelevant.  Calls that may run at the same time (other
+ * streams, graphs replayed side by side) need a workspace and a record each. */
+#define ZS_NORM_WORKSPACE_BYTES 65536
+
+/*
+ * Norm of a shard's reduced gradient: S = sum over i in [0, n) of g_i^2 with
+ * g_i the gradient a step on these partials and this grad_scale would use,
+ *   g_i = (((f32(G[0][i]) + f32(G[1][i])) + ...) + f32(G[k-1][i])) * grad_scale
+ * in binary32 (zs_grad_norm: bf16 partials as in zs_shard_step;
+ * zs_grad_norm_q8grad: int8 partials and scales as in zs_shard_step_q8grad).
+ *
+ *   grads, qgrads, qscales : as for the step, the same alignment
+ *   grad_scale : finite
+ *   rule       : HOST struct or NULL, read during the call only
+ *   clip       : DEVICE record, written whole
+ *   workspace  : see above
+ * The record and the workspace must not overlap each other or a partial
+ * (ZS_ERR_ALIASING).  n == 0 gives S = 0.  Errors are reported synchronously
+ * with nothing enqueued; the arguments are checked before the state of the
+ * library.  HBM traffic: 2kn bytes read (int8: k (n + 4 ceil(n / 256))).
+ */
+int zs_grad_norm(const uint16_t *const *grads, int k, int64_t n, float grad_scale,
+                 const zs_clip_rule *rule, zs_clip *clip, void *workspace, void *stream);
+int zs_grad_norm_q8grad(const int8_t *const *qgrads, const float *const *qscales, int k, int64_t n,
+                        float grad_scale, const zs_clip_rule *rule, zs_clip *clip,
+                        void *workspace, void *stream);
+
+/*
+ * Norm and coefficient of a total: S = the sum of `count` sums of squares
+ * (DEVICE binary64, 8-byte aligned, 1 <= count <= ZS_MAX_SUMS), for instance
+ * what an all-gather of the ranks' records' sumsq delivered, or with count 1
+ * the record's own sumsq after an all-reduce (sumsq may be &clip->sumsq; any
+ * other overlap with the record is ZS_ERR_ALIASING).
+ */
+#define ZS_MAX_SUMS 65536
+int zs_clip_combine(const double *sumsq, int count, const zs_clip_rule *rule, zs_clip *clip,
+                    void *stream);
+
+/*
+ * Lists of tensors: gradients that live outside a flat shard (replicated
+ * parameters, a model without sharding).  zs_tensor_pieces cuts a HOST list of
+ * tensors into pieces, which the caller copies to DEVICE memory once and uses
+ * for as many calls as the tensors stay where they are.
+ */
+#define ZS_DTYPE_BF16 0
+#define ZS_DTYPE_FP16 1
+#define ZS_DTYPE_FP32 2
+
+typedef struct {
+    void *data;       /* DEVICE, n dense elements, aligned to the element's size */
+    int64_t n;        /* >= 0 */
+    int32_t dtype;    /* ZS_DTYPE_* */
+    int32_t reserved; /* must be 0 */
+} zs_tensor;
+
+typedef struct {
+    uint64_t addr;
+    uint32_t n;     /* elements */
+    uint32_t dtype;
+} zs_piece;
+
+/* pieces: DEVICE copy of what zs_tensor_pieces wrote, 16-byte aligned; the
+ * kernels trust its contents, so the tensors must still be where they were. */
+typedef struct {
+    const zs_piece *pieces;
+    int64_t count;
+} zs_tensor_table;
+
+/* Cut `count` tensors (HOST array) into pieces: writes them to pieces[0 ..
+ * *npieces - 1] (HOST, room for `capacity`) in the order of the list; with
+ * pieces NULL only *npieces is set.  Host-only; needs no device and no
+ * zs_init.  ZS_ERR_INVALID_ARGUMENT: a null pointer, a negative size, a null
+ * tensor with elements, an unknown dtype, or capacity too small (*npieces is
+ * then what is needed).  ZS_ERR_MISALIGNED: a tensor not aligned to its element.
+ * ZS_ERR_ALIASING: two tensors overlap (one listed twice would be scaled twice).
+ * ZS_ERR_DEVICE: no host memory for the overlap check. */
+int zs_tensor_pieces(const zs_tensor *tensors, int64_t count, zs_piece *pieces, int64_t capacity,
+                     int64_t *npieces);
+
+/* Norm over every element of the table's tensors: S = sum of x^2.  Record and
+ * workspace as for zs_grad_norm, apart from the tensors.  count == 0 gives
+ * S = 0.  HBM traffic: the tensors once. */
+int zs_tensors_norm(const zs_tensor_table *table, const zs_clip_rule *rule, zs_clip *clip,
+                    void *workspace, void *stream);
+
+/* Scale every element of the table's tensors in place by clip->coef: x becomes
+ * f32(x) * coef rounded once to the tensor's type (to nearest even; NaN ->
+ * 0x7FC0 in bf16).  With apply 0 or coef exactly 1 nothing is read or written
+ * (x * 1 = x).  HBM traffic: the tensors read and written once. */
+int zs_tensors_clip(const zs_tensor_table *table, const zs_clip *clip, void *stream);
+
 /* Release what zs_init recorded.  Later calls return ZS_ERR_NOT_INITIALIZED
  * until zs_init is called again.  Always returns ZS_OK. */
 int zs_fini(void);

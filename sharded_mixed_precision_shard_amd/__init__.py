@@ -11,7 +11,9 @@ Entry points keep the C names: :func:`zs_init`, :func:`zs_shard_step`,
 :func:`zs_shard_step_packed_q8ag`, :func:`zs_shard_step_packed_q8grad`,
 :func:`zs_shard_step_packed_bf16mv`, :func:`zs_shard_step_bf16mv_sr`,
 :func:`zs_shard_step_packed_bf16mv_sr`, :func:`zs_pack_state`, :func:`zs_unpack_state`,
-:func:`zs_pack_state_bf16mv`, :func:`zs_unpack_state_bf16mv`, :func:`zs_fini`,
+:func:`zs_pack_state_bf16mv`, :func:`zs_unpack_state_bf16mv`, :func:`zs_grad_norm`,
+:func:`zs_grad_norm_q8grad`, :func:`zs_clip_combine`, :func:`zs_tensor_pieces`,
+:func:`zs_tensors_norm`, :func:`zs_tensors_clip`, :func:`zs_fini`,
 :func:`zs_status_string`, :func:`zs_last_device_error`, :func:`zs_algorithmic_bytes`,
 :func:`zs_launch_geometry`, :func:`zs_launch_plan`.
 """
@@ -28,6 +30,10 @@ ZS_MAX_K = 16
 ZS_MAX_SEGMENTS = 65536
 ZS_Q8_BLOCK = 256
 ZS_MAX_GROUPS_PER_CU = 32
+ZS_NORM_WORKSPACE_BYTES = 65536
+ZS_MAX_SUMS = 65536
+
+ZS_DTYPE = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
 
 ZS_OK = 0
 ZS_ERR_NOT_INITIALIZED = 1
@@ -46,8 +52,9 @@ EXPORTS = ("zs_init", "zs_shard_step", "zs_shard_step_cfg", "zs_shard_step_q8ag"
            "zs_shard_step_packed_q8ag", "zs_shard_step_packed_q8grad",
            "zs_shard_step_packed_bf16mv", "zs_shard_step_bf16mv_sr",
            "zs_shard_step_packed_bf16mv_sr", "zs_pack_state", "zs_unpack_state",
-           "zs_pack_state_bf16mv", "zs_unpack_state_bf16mv", "zs_fini", "zs_status_string",
-           "zs_last_device_error", "zs_algorithmic_bytes", "zs_launch_geometry",
+           "zs_pack_state_bf16mv", "zs_unpack_state_bf16mv", "zs_grad_norm",
+           "zs_grad_norm_q8grad", "zs_clip_combine", "zs_tensor_pieces", "zs_tensors_norm",
+           "zs_tensors_clip", "zs_fini", "zs_status_string", "zs_last_device_error", "zs_algorithmic_bytes", "zs_launch_geometry",
            "zs_launch_plan")
 
 
@@ -87,6 +94,30 @@ class ZsLaunchInfo(ctypes.Structure):
     _fields_ = [("workgroups", ctypes.c_int64), ("chunk_elements", ctypes.c_int64),
                 ("block_order", ctypes.c_int32), ("groups_per_cu", ctypes.c_int32),
                 ("nontemporal", ctypes.c_int32), ("window_quads", ctypes.c_int32)]
+
+
+class ZsClip(ctypes.Structure):
+    """Layout of the device record (see ClipRecord)."""
+    _fields_ = [("sumsq", ctypes.c_double), ("norm", ctypes.c_float), ("coef", ctypes.c_float),
+                ("apply", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ZsClipRule(ctypes.Structure):
+    _fields_ = [("max_norm", ctypes.c_float), ("eps", ctypes.c_float),
+                ("skip_nonfinite", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ZsTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ZsPiece(ctypes.Structure):
+    _fields_ = [("addr", ctypes.c_uint64), ("n", ctypes.c_uint32), ("dtype", ctypes.c_uint32)]
+
+
+class ZsTensorTable(ctypes.Structure):
+    _fields_ = [("pieces", ctypes.c_void_p), ("count", ctypes.c_int64)]
 
 
 class ZsError(RuntimeError):
@@ -148,6 +179,19 @@ def load_library():
     lib.zs_pack_state.restype = ctypes.c_int
     lib.zs_unpack_state.argtypes = [P, P, P, P, ctypes.c_int64, P]
     lib.zs_unpack_state.restype = ctypes.c_int
+    lib.zs_grad_norm.argtypes = [P, ctypes.c_int, ctypes.c_int64, ctypes.c_float, P, P, P, P]
+    lib.zs_grad_norm.restype = ctypes.c_int
+    lib.zs_grad_norm_q8grad.argtypes = [P, P, ctypes.c_int, ctypes.c_int64, ctypes.c_float, P, P,
+                                        P, P]
+    lib.zs_grad_norm_q8grad.restype = ctypes.c_int
+    lib.zs_clip_combine.argtypes = [P, ctypes.c_int, P, P, P]
+    lib.zs_clip_combine.restype = ctypes.c_int
+    lib.zs_tensor_pieces.argtypes = [P, ctypes.c_int64, P, ctypes.c_int64, P]
+    lib.zs_tensor_pieces.restype = ctypes.c_int
+    lib.zs_tensors_norm.argtypes = [P, P, P, P, P]
+    lib.zs_tensors_norm.restype = ctypes.c_int
+    lib.zs_tensors_clip.argtypes = [P, P, P]
+    lib.zs_tensors_clip.restype = ctypes.c_int
     lib.zs_fini.argtypes = []
     lib.zs_fini.restype = ctypes.c_int
     lib.zs_status_string.argtypes = [ctypes.c_int]
@@ -686,6 +730,229 @@ class ShardStep:
         if check and rc != ZS_OK:
             raise ZsError(rc, "ShardStep(%s)" % self.variant)
         return rc
+
+
+# ------------------------------------------- gradient norm and clipping
+
+def clip_rule(max_norm, eps=1e-6, skip_nonfinite=False) -> ZsClipRule:
+    """The clipping rule: coef = 1 where norm + eps <= max_norm, else
+    max_norm / (norm + eps); ``skip_nonfinite`` makes the clipped step and
+    zs_tensors_clip leave everything as it was when the norm is not finite."""
+    return ZsClipRule(max_norm, eps, 1 if skip_nonfinite else 0, 0)
+
+
+class ClipRecord:
+    """A device record (zs_clip) that a norm call writes and a clipped step or
+    zs_tensors_clip reads: one-element views ``sumsq`` (float64), ``norm``,
+    ``coef`` (float32) and ``apply`` (int32) of it.  Reading one on the host
+    waits for the GPU; an all-reduce of ``sumsq`` and zs_clip_combine do not.
+    Until the first norm call ``apply`` is 0, so nothing is clipped or stepped."""
+
+    def __init__(self, device="cuda"):
+        import torch
+        self.buffer = torch.zeros(ctypes.sizeof(ZsClip), dtype=torch.uint8, device=device)
+        self.sumsq = self.buffer[0:8].view(torch.float64)
+        self.norm = self.buffer[8:12].view(torch.float32)
+        self.coef = self.buffer[12:16].view(torch.float32)
+        self.apply = self.buffer[16:20].view(torch.int32)
+
+
+def norm_workspace(device="cuda"):
+    """Workspace of a norm call; calls that may overlap in time need one each."""
+    import torch
+    return torch.empty(ZS_NORM_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+
+
+def _record(clip) -> int:
+    return _dev(clip.buffer if isinstance(clip, ClipRecord) else clip, ctypes.sizeof(ZsClip),
+                "clip")
+
+
+def _rule(rule):
+    if rule is not None and not isinstance(rule, ZsClipRule):
+        raise TypeError("rule: expected a ZsClipRule (see clip_rule) or None, got %r"
+                        % (type(rule),))
+    return None if rule is None else ctypes.byref(rule)
+
+
+def _same_device(xs):
+    """The device index the given tensors share (None if none of them says)."""
+    devices = [getattr(x.buffer if isinstance(x, ClipRecord) else x, "device", None) for x in xs]
+    found = {d.index for d in devices if isinstance(getattr(d, "index", None), int)}
+    if len(found) > 1:
+        raise ValueError("buffers on different devices: %s" % sorted(found))
+    return found.pop() if found else None
+
+
+def _on_device(index):
+    """Refuse a call on buffers of a device that is not the current one."""
+    if index is not None:
+        import torch
+        if torch.cuda.current_device() != index:
+            raise ValueError("the buffers are on device %d, the current device is %d"
+                             % (index, torch.cuda.current_device()))
+
+
+class GradNorm:
+    """The norm call on a shard's partials with its buffers fixed: checked and
+    marshalled once, as ShardStep does for the step.  ``partials`` are bf16
+    [n], or int8 [n] with their block scales ``qscales``; ``rule`` is a
+    clip_rule or None; ``clip`` the record it writes.  The workspace is its own
+    unless one is given."""
+
+    def __init__(self, partials, n, rule, clip, grad_scale=1.0, qscales=None, workspace=None):
+        lib = load_library()
+        n = int(n)
+        nn = max(n, 0)
+        if qscales is not None and len(qscales) != len(partials):
+            raise ValueError("%d qscales for %d partials: one scale array per int8 partial"
+                             % (len(qscales), len(partials)))
+        self._device = _same_device([*partials, *(qscales or []), clip, workspace])
+        if workspace is None:
+            workspace = norm_workspace("cuda" if self._device is None else self._device)
+        self._keep = [list(partials), qscales, rule, clip, workspace]
+        if qscales is None:
+            self._c = (_ptr_array(partials, 2 * nn, "grads"),)
+            self._fn, self._name = lib.zs_grad_norm, "zs_grad_norm"
+        else:
+            self._c = (_ptr_array(partials, nn, "qgrads"),
+                       _ptr_array(qscales, 4 * -(-nn // ZS_Q8_BLOCK), "qscales"))
+            self._fn, self._name = lib.zs_grad_norm_q8grad, "zs_grad_norm_q8grad"
+        self._args = [*(ctypes.cast(c, ctypes.c_void_p) for c in self._c), len(partials), n,
+                      float(grad_scale), _rule(rule), _record(clip),
+                      _dev(workspace, ZS_NORM_WORKSPACE_BYTES, "workspace")]
+
+    def __call__(self, stream=None, check=True) -> int:
+        _on_device(self._device)
+        rc = self._fn(*self._args, _stream_handle(stream))
+        if check and rc != ZS_OK:
+            raise ZsError(rc, self._name)
+        return rc
+
+
+def zs_grad_norm(grads, k, n, grad_scale, rule, clip, workspace, stream=None, check=True) -> int:
+    """Enqueue the norm of the reduced gradient of k bf16 partials (see include/zs.h)."""
+    _check_k(k, grads, "grads")
+    return GradNorm(grads, n, rule, clip, grad_scale, None, workspace)(stream, check)
+
+
+def zs_grad_norm_q8grad(qgrads, qscales, k, n, grad_scale, rule, clip, workspace, stream=None,
+                        check=True) -> int:
+    """zs_grad_norm on int8 partials and their block scales."""
+    _check_k(k, qgrads, "qgrads")
+    return GradNorm(qgrads, n, rule, clip, grad_scale, qscales, workspace)(stream, check)
+
+
+def zs_clip_combine(sumsq, rule, clip, stream=None, count=None, check=True) -> int:
+    """Norm and coefficient of the sum of ``sumsq`` (device float64 [count]), for
+    instance the ranks' gathered sums, or the record's own after an all-reduce."""
+    if not isinstance(sumsq, int):
+        if str(getattr(sumsq, "dtype", "")) not in ("", "torch.float64"):
+            raise TypeError("sumsq must be float64, got %s" % sumsq.dtype)
+        count = sumsq.numel() if count is None else count
+    args = [_dev(sumsq, 8 * max(int(count), 0), "sumsq"), int(count), _rule(rule), _record(clip)]
+    _on_device(_same_device([sumsq, clip]))
+    rc = load_library().zs_clip_combine(*args, _stream_handle(stream))
+    if check and rc != ZS_OK:
+        raise ZsError(rc, "zs_clip_combine")
+    return rc
+
+
+def _dense(x) -> bool:
+    """Whether a tensor's elements fill one stretch of memory, in any order of
+    its dimensions (a transposed weight's gradient, say)."""
+    if x.is_contiguous():
+        return True
+    want = 1
+    for stride, size in sorted((st, sz) for st, sz in zip(x.stride(), x.shape) if sz != 1):
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def zs_tensor_pieces(tensors):
+    """Host array of the pieces of a list of (address, n, dtype code) or of GPU
+    tensors (see include/zs.h): what a zs_tensor_table's device memory holds."""
+    arr = (ZsTensor * max(len(tensors), 1))()
+    for i, x in enumerate(tensors):
+        if isinstance(x, tuple):
+            arr[i].data, arr[i].n, arr[i].dtype = (int(y) for y in x)
+            continue
+        name = "tensors[%d]" % i
+        if not getattr(x, "is_cuda", False):
+            raise ValueError("%s must be a GPU tensor" % name)
+        if str(x.dtype) not in ZS_DTYPE:
+            raise TypeError("%s: %s is not bfloat16, float16 or float32" % (name, x.dtype))
+        if not _dense(x):
+            raise ValueError("%s must be dense: its elements without gaps or repeats" % name)
+        arr[i].data, arr[i].n, arr[i].dtype = x.data_ptr(), x.numel(), ZS_DTYPE[str(x.dtype)]
+    lib = load_library()
+    made = ctypes.c_int64(0)
+    rc = lib.zs_tensor_pieces(arr, len(tensors), None, 0, ctypes.byref(made))
+    if rc == ZS_OK:
+        out = (ZsPiece * made.value)()
+        if made.value == 0:
+            return out
+        rc = lib.zs_tensor_pieces(arr, len(tensors), out, made.value, ctypes.byref(made))
+    if rc != ZS_OK:
+        raise ZsError(rc, "zs_tensor_pieces")
+    return out
+
+
+class TensorTable:
+    """A list of GPU tensors (bf16, fp16 and fp32 mixed; dense, any alignment)
+    for zs_tensors_norm and zs_tensors_clip.  Its pieces are copied to the
+    device here, on the current stream; the tensors are referenced for the
+    object's lifetime and must keep their memory (no resize, no new ``.data``)."""
+
+    def __init__(self, tensors):
+        import torch
+        tensors = list(tensors)
+        pieces = zs_tensor_pieces(tensors)
+        self.device = _same_device(tensors)
+        self.tensors = tensors
+        self.buffer = None
+        if len(pieces):
+            host = torch.frombuffer(pieces, dtype=torch.uint8)
+            self.buffer = host.to(torch.device("cuda", self.device))
+        self.table = ZsTensorTable(_dev(self.buffer, ctypes.sizeof(pieces), "pieces"), len(pieces))
+
+
+class TensorsNorm:
+    """The norm call on a TensorTable with its arguments fixed; the workspace is
+    its own unless one is given."""
+
+    def __init__(self, table, rule, clip, workspace=None):
+        self._device = _same_device([clip, workspace, *table.tensors[:1]])
+        if workspace is None:
+            workspace = norm_workspace("cuda" if self._device is None else self._device)
+        self._keep = [table, rule, clip, workspace]
+        self._fn = load_library().zs_tensors_norm
+        self._args = [ctypes.byref(table.table), _rule(rule), _record(clip),
+                      _dev(workspace, ZS_NORM_WORKSPACE_BYTES, "workspace")]
+
+    def __call__(self, stream=None, check=True) -> int:
+        _on_device(self._device)
+        rc = self._fn(*self._args, _stream_handle(stream))
+        if check and rc != ZS_OK:
+            raise ZsError(rc, "zs_tensors_norm")
+        return rc
+
+
+def zs_tensors_norm(table, rule, clip, workspace, stream=None, check=True) -> int:
+    """Enqueue the norm over a TensorTable's tensors (see include/zs.h)."""
+    return TensorsNorm(table, rule, clip, workspace)(stream, check)
+
+
+def zs_tensors_clip(table, clip, stream=None, check=True) -> int:
+    """Enqueue the scaling of a TensorTable's tensors by the record's coef, in place."""
+    _on_device(_same_device([clip, *table.tensors[:1]]))
+    rc = load_library().zs_tensors_clip(ctypes.byref(table.table), _record(clip),
+                                        _stream_handle(stream))
+    if check and rc != ZS_OK:
+        raise ZsError(rc, "zs_tensors_clip")
+    return rc
 
 
 def algorithmic_bytes(variant: str, k: int, n: int) -> int:

@@ -1,17 +1,21 @@
 // zs_api.hip -- the C ABI declared in include/zs.h: argument checks, launch
-// geometry and the launch of the shard step kernels (zs_kernels.hip).
+// geometry and the launch of the shard step kernels (zs_kernels.hip) and of the
+// norm and scaling kernels (zs_norm.hip).
 //
 // Errors are found on the host before anything is enqueued; the library
 // allocates nothing and keeps no pointer after a call returns.
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <new>
 
 #include "zs.h"
 #include "zs_kernels.h"
+#include "zs_norm.h"
 
 namespace {
 
@@ -333,6 +337,102 @@ int layout_call(int dir, bool mv16, float *master, void *m, void *v, float *stat
     return ZS_OK;
 }
 
+// The device a call runs on, prepared by zs_init.
+int current_device(int *dev) {
+    if (!g_initialized) return ZS_ERR_NOT_INITIALIZED;
+    const hipError_t e = hipGetDevice(dev);
+    if (e != hipSuccess) return device_error(e);
+    if (*dev < 0 || *dev >= kMaxDevices || !g_dev[*dev].ready) return ZS_ERR_NOT_INITIALIZED;
+    return ZS_OK;
+}
+
+// The clipping rule and the record a norm call writes.
+int check_rule(const zs_clip_rule *rule, const zs_clip *clip, Rule *out) {
+    out->max_norm = INFINITY;
+    out->eps = 0.0f;
+    out->skip_nonfinite = 0;
+    if (rule) {
+        if (!(rule->max_norm >= 0.0f) || !(rule->eps >= 0.0f) || !std::isfinite(rule->eps) ||
+            rule->reserved != 0)
+            return ZS_ERR_INVALID_ARGUMENT;
+        out->max_norm = rule->max_norm;
+        out->eps = rule->eps;
+        out->skip_nonfinite = rule->skip_nonfinite != 0;
+    }
+    if (!clip) return ZS_ERR_INVALID_ARGUMENT;
+    if ((uintptr_t)clip & 7u) return ZS_ERR_MISALIGNED;
+    return ZS_OK;
+}
+
+int check_workspace(const zs_clip *clip, const void *workspace) {
+    if (!workspace) return ZS_ERR_INVALID_ARGUMENT;
+    if ((uintptr_t)workspace & 7u) return ZS_ERR_MISALIGNED;
+    if (overlaps(clip, sizeof(zs_clip), workspace, ZS_NORM_WORKSPACE_BYTES)) return ZS_ERR_ALIASING;
+    return ZS_OK;
+}
+
+// Workgroups of a launch over `want` workgroups' worth of work, each looping
+// over its share: enough to fill the device.
+int fill_blocks(int dev, int64_t want) {
+    const int64_t fill = std::min((int64_t)g_dev[dev].cus * 16, kMaxSums);
+    return (int)std::min(want, fill);
+}
+
+int norm_call(bool q8, const uint16_t *const *grads, const int8_t *const *qgrads,
+              const float *const *qscales, int k, int64_t n, float grad_scale,
+              const zs_clip_rule *rule, zs_clip *clip, void *workspace, void *stream) {
+    if (k < 1 || k > ZS_MAX_K || n < 0 || n > INT64_MAX / 8 || !std::isfinite(grad_scale))
+        return ZS_ERR_INVALID_ARGUMENT;
+    Rule r;
+    int st = check_rule(rule, clip, &r);
+    if (st == ZS_OK) st = check_workspace(clip, workspace);
+    if (st != ZS_OK) return st;
+    if (q8 ? (!qgrads || !qscales) : !grads) return ZS_ERR_INVALID_ARGUMENT;
+    NormArgs a = {};
+    if (n > 0) {
+        const int64_t nblocks = (n + kQ8Block - 1) / kQ8Block;
+        Span ins[2 * ZS_MAX_K];
+        int nins = 0;
+        for (int j = 0; j < k; ++j) {
+            if (q8) {
+                ins[nins++] = {a.qgrads[j] = qgrads[j], n, 16};
+                ins[nins++] = {a.qscales[j] = qscales[j], 4 * nblocks, 4};
+            } else {
+                ins[nins++] = {a.grads[j] = grads[j], 2 * n, 16};
+            }
+        }
+        for (int x = 0; x < nins; ++x)
+            if (!ins[x].p) return ZS_ERR_INVALID_ARGUMENT;
+        for (int x = 0; x < nins; ++x)
+            if ((uintptr_t)ins[x].p & (ins[x].align - 1)) return ZS_ERR_MISALIGNED;
+        for (int x = 0; x < nins; ++x)
+            if (overlaps(clip, sizeof(zs_clip), ins[x].p, ins[x].bytes) ||
+                overlaps(workspace, ZS_NORM_WORKSPACE_BYTES, ins[x].p, ins[x].bytes))
+                return ZS_ERR_ALIASING;
+    }
+    int dev = 0;
+    st = current_device(&dev);
+    if (st != ZS_OK) return st;
+    a.n = n;
+    a.gscale = grad_scale;
+    a.sums = (double *)workspace;
+    const int blocks = fill_blocks(dev, (n + kThreads - 1) / kThreads);
+    if (blocks > 0) {
+        const hipError_t e = launch_grad_norm(k, q8, a, blocks, (hipStream_t)stream);
+        if (e != hipSuccess) return device_error(e);
+    }
+    const hipError_t e = launch_finish(a.sums, blocks, r, clip, (hipStream_t)stream);
+    return e == hipSuccess ? ZS_OK : device_error(e);
+}
+
+int check_table(const zs_tensor_table *table) {
+    if (!table || table->count < 0 || table->count > INT64_MAX / (int64_t)sizeof(zs_piece) ||
+        (table->count > 0 && !table->pieces))
+        return ZS_ERR_INVALID_ARGUMENT;
+    if ((uintptr_t)table->pieces & 15u) return ZS_ERR_MISALIGNED;
+    return ZS_OK;
+}
+
 Request base_request(float *master, void *m, void *v, uint16_t *param, int k, int64_t n,
                      const zs_seg_table *st, const zs_hparams *hp, int64_t step, void *stream) {
     Request r;
@@ -522,6 +622,125 @@ int zs_unpack_state_bf16mv(const float *state, float *master, uint16_t *m_bf16, 
                            int64_t n, void *stream) {
     return layout_call(kLayoutUnpack, true, master, m_bf16, v_bf16, const_cast<float *>(state), n,
                        stream);
+}
+
+int zs_grad_norm(const uint16_t *const *grads, int k, int64_t n, float grad_scale,
+                 const zs_clip_rule *rule, zs_clip *clip, void *workspace, void *stream) {
+    return norm_call(false, grads, nullptr, nullptr, k, n, grad_scale, rule, clip, workspace,
+                     stream);
+}
+
+int zs_grad_norm_q8grad(const int8_t *const *qgrads, const float *const *qscales, int k, int64_t n,
+                        float grad_scale, const zs_clip_rule *rule, zs_clip *clip,
+                        void *workspace, void *stream) {
+    return norm_call(true, nullptr, qgrads, qscales, k, n, grad_scale, rule, clip, workspace,
+                     stream);
+}
+
+int zs_clip_combine(const double *sumsq, int count, const zs_clip_rule *rule, zs_clip *clip,
+                    void *stream) {
+    Rule r;
+    int st = check_rule(rule, clip, &r);
+    if (st != ZS_OK) return st;
+    if (!sumsq || count < 1 || count > ZS_MAX_SUMS) return ZS_ERR_INVALID_ARGUMENT;
+    if ((uintptr_t)sumsq & 7u) return ZS_ERR_MISALIGNED;
+    if (overlaps(sumsq, (int64_t)sizeof(double) * count, clip, sizeof(zs_clip)) &&
+        !(count == 1 && sumsq == &clip->sumsq))
+        return ZS_ERR_ALIASING;
+    int dev = 0;
+    st = current_device(&dev);
+    if (st != ZS_OK) return st;
+    const hipError_t e = launch_finish(sumsq, count, r, clip, (hipStream_t)stream);
+    return e == hipSuccess ? ZS_OK : device_error(e);
+}
+
+int zs_tensor_pieces(const zs_tensor *tensors, int64_t count, zs_piece *pieces, int64_t capacity,
+                     int64_t *npieces) {
+    if (!npieces || count < 0 || (count > 0 && !tensors)) return ZS_ERR_INVALID_ARGUMENT;
+    for (int64_t i = 0; i < count; ++i) {
+        const zs_tensor &x = tensors[i];
+        if (x.n < 0 || x.n > INT64_MAX / 8 || x.dtype < ZS_DTYPE_BF16 || x.dtype > ZS_DTYPE_FP32 ||
+            x.reserved != 0 || (x.n > 0 && !x.data))
+            return ZS_ERR_INVALID_ARGUMENT;
+        const uint64_t size = (uint64_t)dtype_size((uint32_t)x.dtype);
+        if (x.n > 0 && (uintptr_t)x.data % size) return ZS_ERR_MISALIGNED;
+        if ((uintptr_t)x.data > UINT64_MAX - (uint64_t)x.n * size) return ZS_ERR_INVALID_ARGUMENT;
+    }
+    // no two tensors overlap: in the order of their addresses each ends before the next
+    struct Range {
+        uintptr_t a, b;
+    };
+    Range *ranges = count > 0 ? new (std::nothrow) Range[(size_t)count] : nullptr;
+    if (count > 0 && !ranges) return device_error(hipErrorOutOfMemory);
+    int64_t used = 0;
+    for (int64_t i = 0; i < count; ++i)
+        if (tensors[i].n > 0) {
+            const uintptr_t a = (uintptr_t)tensors[i].data;
+            ranges[used++] = {a, a + (uintptr_t)(tensors[i].n * dtype_size(tensors[i].dtype))};
+        }
+    std::sort(ranges, ranges + used, [](const Range &x, const Range &y) { return x.a < y.a; });
+    bool clear = true;
+    for (int64_t i = 1; i < used; ++i) clear = clear && ranges[i - 1].b <= ranges[i].a;
+    delete[] ranges;
+    if (!clear) return ZS_ERR_ALIASING;
+
+    int64_t made = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const uint32_t dtype = (uint32_t)tensors[i].dtype;
+        uint64_t a = (uint64_t)(uintptr_t)tensors[i].data;
+        const uint64_t end = a + (uint64_t)tensors[i].n * dtype_size(dtype);
+        while (a < end) {
+            const uint64_t cut = std::min(end, (a / kPieceBytes + 1) * (uint64_t)kPieceBytes);
+            if (pieces && made < capacity)
+                pieces[made] = {a, (uint32_t)((cut - a) / dtype_size(dtype)), dtype};
+            ++made;
+            a = cut;
+        }
+    }
+    *npieces = made;
+    return pieces && made > capacity ? ZS_ERR_INVALID_ARGUMENT : ZS_OK;
+}
+
+int zs_tensors_norm(const zs_tensor_table *table, const zs_clip_rule *rule, zs_clip *clip,
+                    void *workspace, void *stream) {
+    Rule r;
+    int st = check_table(table);
+    if (st == ZS_OK) st = check_rule(rule, clip, &r);
+    if (st == ZS_OK) st = check_workspace(clip, workspace);
+    if (st != ZS_OK) return st;
+    const int64_t bytes = (int64_t)sizeof(zs_piece) * table->count;
+    if (overlaps(clip, sizeof(zs_clip), table->pieces, bytes) ||
+        overlaps(workspace, ZS_NORM_WORKSPACE_BYTES, table->pieces, bytes))
+        return ZS_ERR_ALIASING;
+    int dev = 0;
+    st = current_device(&dev);
+    if (st != ZS_OK) return st;
+    const int blocks =
+        fill_blocks(dev, (table->count + kThreads / kWave - 1) / (kThreads / kWave));
+    double *const sums = (double *)workspace;
+    if (blocks > 0) {
+        const hipError_t e = launch_tensors_norm(table->pieces, table->count, sums, blocks,
+                                                 (hipStream_t)stream);
+        if (e != hipSuccess) return device_error(e);
+    }
+    const hipError_t e = launch_finish(sums, blocks, r, clip, (hipStream_t)stream);
+    return e == hipSuccess ? ZS_OK : device_error(e);
+}
+
+int zs_tensors_clip(const zs_tensor_table *table, const zs_clip *clip, void *stream) {
+    int st = check_table(table);
+    if (st != ZS_OK) return st;
+    if (!clip) return ZS_ERR_INVALID_ARGUMENT;
+    if ((uintptr_t)clip & 7u) return ZS_ERR_MISALIGNED;
+    int dev = 0;
+    st = current_device(&dev);
+    if (st != ZS_OK) return st;
+    const int blocks =
+        fill_blocks(dev, (table->count + kThreads / kWave - 1) / (kThreads / kWave));
+    if (blocks == 0) return ZS_OK;
+    const hipError_t e = launch_tensors_clip(table->pieces, table->count, clip, blocks,
+                                             (hipStream_t)stream);
+    return e == hipSuccess ? ZS_OK : device_error(e);
 }
 
 int zs_fini(void) {
