@@ -495,8 +495,8 @@ int zs_tensors_norm(const zs_tensor_table *table, const zs_clip_rule *rule, zs_c
                     void *workspace, void *stream);
 
 /* Scale every element of the table's tensors in place by clip->coef: x becomes
- * f32(x) * coef rounded once to the tensor's type (to nearest even; NaN ->
- * 0x7FC0 in bf16).  With apply 0 or coef exactly 1 nothing is read or written
+ * f32(x) * coef in binary32, rounded to the tensor's type (to nearest even; NaN
+ * -> 0x7FC0 in bf16).  With apply 0 or coef exactly 1 nothing is read or written
  * (x * 1 = x).  HBM traffic: the tensors read and written once. */
 int zs_tensors_clip(const zs_tensor_table *table, const zs_clip *clip, void *stream);
 
