@@ -409,8 +409,9 @@ typedef struct {
 } zs_clip_rule;
 
 /* Bytes of workspace a norm call needs: DEVICE memory of the caller, 8-byte
- * aligned, contents irrelevant.  Calls that may run at the same time (other
- * streams, graphs replayed side by side) need a workspace and a record each. */
+ * aligned, set to zero once before its first call (each call leaves it ready
+ * for the next).  Calls that may run at the same time (other streams, graphs
+ * replayed side by side) need a workspace and a record each. */
 #define ZS_NORM_WORKSPACE_BYTES 65536
 
 /*
@@ -446,6 +447,38 @@ int zs_grad_norm_q8grad(const int8_t *const *qgrads, const float *const *qscales
 #define ZS_MAX_SUMS 65536
 int zs_clip_combine(const double *sumsq, int count, const zs_clip_rule *rule, zs_clip *clip,
                     void *stream);
+
+/*
+ * A shard step on the clipped gradient: the step of entry point `variant`
+ * (ZS_VARIANT_*, below) with grad_scale replaced by the binary32 product
+ * hparams->grad_scale * clip->coef, read from the device record when the
+ * kernel runs.  With coef 1 every output bit is the unclipped step's.  A record
+ * with apply 0 skips the step: no buffer changes (the caller's step count t
+ * went up all the same).  The record a norm call on the same partials,
+ * grad_scale and stream wrote just before is the usual one; it is read only.
+ *
+ *   buffers : HOST struct of what the entry point takes, the rest unused (for
+ *             the packed forms `master` is the state)
+ *   seed    : for the _SR variants, otherwise ignored
+ *   clip    : DEVICE record, 8-byte aligned, apart from every output
+ * Everything else, errors and HBM traffic as for the entry point; the record
+ * is one more read per workgroup.  Capturing the norm call and the step into
+ * one graph makes every replay clip by the norm of that replay's gradient.
+ */
+typedef struct {
+    float *master;
+    void *m;
+    void *v;
+    uint16_t *param_bf16;
+    int8_t *param_q8;
+    float *param_q8_scale;
+    const uint16_t *const *grads;
+    const int8_t *const *qgrads;
+    const float *const *qscales;
+} zs_step_buffers;
+int zs_shard_step_clipped(int variant, const zs_step_buffers *buffers, int k, int64_t n,
+                          const zs_seg_table *seg_table, const zs_hparams *hparams, int64_t step,
+                          uint64_t seed, const zs_clip *clip, void *stream);
 
 /*
  * Lists of tensors: gradients that live outside a flat shard (replicated

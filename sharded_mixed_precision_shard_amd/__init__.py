@@ -12,8 +12,8 @@ Entry points keep the C names: :func:`zs_init`, :func:`zs_shard_step`,
 :func:`zs_shard_step_packed_bf16mv`, :func:`zs_shard_step_bf16mv_sr`,
 :func:`zs_shard_step_packed_bf16mv_sr`, :func:`zs_pack_state`, :func:`zs_unpack_state`,
 :func:`zs_pack_state_bf16mv`, :func:`zs_unpack_state_bf16mv`, :func:`zs_grad_norm`,
-:func:`zs_grad_norm_q8grad`, :func:`zs_clip_combine`, :func:`zs_tensor_pieces`,
-:func:`zs_tensors_norm`, :func:`zs_tensors_clip`, :func:`zs_fini`,
+:func:`zs_grad_norm_q8grad`, :func:`zs_clip_combine`, :func:`zs_shard_step_clipped`,
+:func:`zs_tensor_pieces`, :func:`zs_tensors_norm`, :func:`zs_tensors_clip`, :func:`zs_fini`,
 :func:`zs_status_string`, :func:`zs_last_device_error`, :func:`zs_algorithmic_bytes`,
 :func:`zs_launch_geometry`, :func:`zs_launch_plan`.
 """
@@ -53,7 +53,7 @@ EXPORTS = ("zs_init", "zs_shard_step", "zs_shard_step_cfg", "zs_shard_step_q8ag"
            "zs_shard_step_packed_bf16mv", "zs_shard_step_bf16mv_sr",
            "zs_shard_step_packed_bf16mv_sr", "zs_pack_state", "zs_unpack_state",
            "zs_pack_state_bf16mv", "zs_unpack_state_bf16mv", "zs_grad_norm",
-           "zs_grad_norm_q8grad", "zs_clip_combine", "zs_tensor_pieces", "zs_tensors_norm",
+           "zs_grad_norm_q8grad", "zs_clip_combine", "zs_shard_step_clipped", "zs_tensor_pieces", "zs_tensors_norm",
            "zs_tensors_clip", "zs_fini", "zs_status_string", "zs_last_device_error", "zs_algorithmic_bytes", "zs_launch_geometry",
            "zs_launch_plan")
 
@@ -105,6 +105,12 @@ class ZsClip(ctypes.Structure):
 class ZsClipRule(ctypes.Structure):
     _fields_ = [("max_norm", ctypes.c_float), ("eps", ctypes.c_float),
                 ("skip_nonfinite", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class ZsStepBuffers(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in (
+        "master", "m", "v", "param_bf16", "param_q8", "param_q8_scale", "grads", "qgrads",
+        "qscales")]
 
 
 class ZsTensor(ctypes.Structure):
@@ -186,6 +192,9 @@ def load_library():
     lib.zs_grad_norm_q8grad.restype = ctypes.c_int
     lib.zs_clip_combine.argtypes = [P, ctypes.c_int, P, P, P]
     lib.zs_clip_combine.restype = ctypes.c_int
+    lib.zs_shard_step_clipped.argtypes = [ctypes.c_int, P, ctypes.c_int, ctypes.c_int64, P, P,
+                                          ctypes.c_int64, ctypes.c_uint64, P, P]
+    lib.zs_shard_step_clipped.restype = ctypes.c_int
     lib.zs_tensor_pieces.argtypes = [P, ctypes.c_int64, P, ctypes.c_int64, P]
     lib.zs_tensor_pieces.restype = ctypes.c_int
     lib.zs_tensors_norm.argtypes = [P, P, P, P, P]
@@ -620,6 +629,20 @@ def zs_unpack_state_bf16mv(state, master, m_bf16, v_bf16, n, stream=None, check=
     return rc
 
 
+_SEPARATE = ("master", "m", "v", "param_bf16")
+_PACKED = ("master", "param_bf16")
+_PAYLOAD = ("param_q8", "param_q8_scale")
+
+# The buffers an entry point takes, in the order of its arguments.
+_STEP_BUFFERS = {
+    "base": (*_SEPARATE, "grads"), "bf16mv": (*_SEPARATE, "grads"),
+    "bf16mv_sr": (*_SEPARATE, "grads"), "q8ag": (*_SEPARATE, *_PAYLOAD, "grads"),
+    "q8grad": (*_SEPARATE, "qgrads", "qscales"), "packed": (*_PACKED, "grads"),
+    "packed_bf16mv": (*_PACKED, "grads"), "packed_bf16mv_sr": (*_PACKED, "grads"),
+    "packed_q8ag": (*_PACKED, *_PAYLOAD, "grads"),
+    "packed_q8grad": (*_PACKED, "qgrads", "qscales")}
+
+
 class ShardStep:
     """One rank's step with its buffers fixed: the arguments are checked and
     marshalled once, and each call passes only the step t and the stream to
@@ -631,12 +654,14 @@ class ShardStep:
     v are bf16) or "packed" (``master`` is the packed state, m and v are None),
     and "packed_q8ag" / "packed_q8grad" / "packed_bf16mv" (those forms on
     their packed state); "bf16mv_sr" and "packed_bf16mv_sr" round the bf16
-    moments stochastically with the random streams of ``seed``.
+    moments stochastically with the random streams of ``seed``.  With ``clip``
+    (a ClipRecord) the step runs on the gradient clipped by the record's
+    coefficient (zs_shard_step_clipped).
     The tensors are referenced for the object's lifetime."""
 
     def __init__(self, master, m, v, param_bf16, grads, n, seg_table_, hparams_,
                  variant="base", param_q8=None, param_q8_scale=None, qscales=None, cfg=None,
-                 seed=None):
+                 seed=None, clip=None):
         lib = load_library()
         # the stochastic forms take the seed between the step and the stream
         self._mid = []
@@ -723,16 +748,45 @@ class ShardStep:
             raise ValueError("a launch cfg applies to the base entry point only")
         self._fn = fn
         self.variant = variant
+        self._device = None
+        self._clipped = clip is not None
+        if self._clipped:
+            if cfg:
+                raise ValueError("a clipped step takes no launch cfg")
+            self._device = _same_device([master, m, v, param_bf16, *grads, param_q8,
+                                         param_q8_scale, *(qscales or []), clip])
+            self._buffers = ZsStepBuffers(**dict(zip(_STEP_BUFFERS[variant], head)))
+            self._keep.append(clip)
+            self._head = [ZS_VARIANT[variant], ctypes.byref(self._buffers), *self._head[len(head):]]
+            self._mid = self._mid or [0]
+            self._tail = [_record(clip)]
+            self._fn = lib.zs_shard_step_clipped
 
     def __call__(self, step, stream=None, check=True) -> int:
-        rc = self._fn(*self._head, int(step), *self._mid,
-                      ctypes.c_void_p(_stream_handle(stream)), *self._tail)
+        if self._device is not None:
+            _on_device(self._device)
+        s = ctypes.c_void_p(_stream_handle(stream))
+        if self._clipped:
+            rc = self._fn(*self._head, int(step), *self._mid, *self._tail, s)
+        else:
+            rc = self._fn(*self._head, int(step), *self._mid, s, *self._tail)
         if check and rc != ZS_OK:
             raise ZsError(rc, "ShardStep(%s)" % self.variant)
         return rc
 
 
 # ------------------------------------------- gradient norm and clipping
+
+def zs_shard_step_clipped(variant, master, m, v, param_bf16, grads, n, seg_table_, hparams_, step,
+                          clip, stream=None, param_q8=None, param_q8_scale=None, qscales=None,
+                          seed=None, check=True) -> int:
+    """The step of entry point ``variant`` on the gradient clipped by the record's
+    coefficient (see include/zs.h); arguments as for ShardStep."""
+    if clip is None:
+        raise ValueError("a clipped step needs a record")
+    return ShardStep(master, m, v, param_bf16, grads, n, seg_table_, hparams_, variant, param_q8,
+                     param_q8_scale, qscales, None, seed, clip)(step, stream, check)
+
 
 def clip_rule(max_norm, eps=1e-6, skip_nonfinite=False) -> ZsClipRule:
     """The clipping rule: coef = 1 where norm + eps <= max_norm, else
@@ -758,9 +812,9 @@ class ClipRecord:
 
 
 def norm_workspace(device="cuda"):
-    """Workspace of a norm call; calls that may overlap in time need one each."""
+    """Workspace of a norm call, zeroed; calls that may overlap in time need one each."""
     import torch
-    return torch.empty(ZS_NORM_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+    return torch.zeros(ZS_NORM_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
 
 
 def _record(clip) -> int:

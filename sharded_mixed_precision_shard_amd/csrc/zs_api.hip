@@ -157,7 +157,17 @@ struct Request {
     const zs_launch_cfg *cfg = nullptr;
     int variant = 0;
     uint64_t seed = 0;  // kSR: the caller's seed of the random streams
+    const zs_clip *clip = nullptr;  // a clipped step's record
 };
+
+// Dynamic LDS that caps a kernel of `used` static bytes at `groups` resident
+// workgroups per compute unit: each reserves that share of the unit's LDS
+// (rounded down to 1 KB; the kernels never touch the reserved bytes).  -1 if
+// the device cannot hold it.
+int64_t cap_lds(int dev, int groups, int64_t used) {
+    const int64_t share = g_dev[dev].lds_per_cu / groups / 1024 * 1024;
+    return share <= g_dev[dev].lds_per_group && share >= used ? share - used : -1;
+}
 
 struct Span {
     const void *p;
@@ -235,12 +245,19 @@ int validate_and_launch(const Request &r) {
             if (overlaps(outs[x].p, outs[x].bytes, ins[y].p, ins[y].bytes)) return ZS_ERR_ALIASING;
     }
 
+    if (r.clip) {
+        if ((uintptr_t)r.clip & 7u) return ZS_ERR_MISALIGNED;
+        for (int x = 0; x < nouts; ++x)
+            if (overlaps(outs[x].p, outs[x].bytes, r.clip, sizeof(zs_clip))) return ZS_ERR_ALIASING;
+    }
+
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return device_error(e);
     if (dev < 0 || dev >= kMaxDevices || !g_dev[dev].ready) return ZS_ERR_NOT_INITIALIZED;
 
     StepArgs a;
+    a.clip = r.clip;
     a.master = r.master;
     a.m = r.m;
     a.v = r.v;
@@ -278,18 +295,13 @@ int validate_and_launch(const Request &r) {
     const bool default_cap = plan.groups_per_cu < 0;
     const int groups_per_cu = default_cap ? -plan.groups_per_cu : plan.groups_per_cu;
 
-    // Occupancy cap: each workgroup reserves 1/groups_per_cu of the unit's
-    // LDS (rounded down to 1 KB), so at most groups_per_cu of them fit.  The
-    // kernels never touch the reserved bytes.
     // A cap the caller asked for and cannot be met is an error; the default
     // cap is simply dropped on a device where it does not fit.
     size_t dyn_lds = 0;
     if (groups_per_cu > 0) {
-        const int64_t share = g_dev[dev].lds_per_cu / groups_per_cu / 1024 * 1024;
-        if (share <= g_dev[dev].lds_per_group && share >= kStaticLds)
-            dyn_lds = (size_t)(share - kStaticLds);
-        else if (!default_cap)
-            return ZS_ERR_INVALID_ARGUMENT;
+        const int64_t lds = cap_lds(dev, groups_per_cu, kStaticLds);
+        if (lds >= 0) dyn_lds = (size_t)lds;
+        else if (!default_cap) return ZS_ERR_INVALID_ARGUMENT;
     }
 
     const int unit_bc = (a.bc1 == 1.0f ? 1 : 0) | (a.bc2 == 1.0f ? 2 : 0);
@@ -371,11 +383,41 @@ int check_workspace(const zs_clip *clip, const void *workspace) {
     return ZS_OK;
 }
 
-// Workgroups of a launch over `want` workgroups' worth of work, each looping
-// over its share: enough to fill the device.
-int fill_blocks(int dev, int64_t want) {
-    const int64_t fill = std::min((int64_t)g_dev[dev].cus * 16, kMaxSums);
-    return (int)std::min(want, fill);
+// Workgroups of a norm launch over `units` workgroups' worth of work, each
+// looping over its share: at most `per_cu` for each compute unit, and all of
+// them the same number of rounds (the last one short).
+int norm_blocks(int dev, int64_t units, int per_cu) {
+    const int64_t fill = std::min((int64_t)g_dev[dev].cus * per_cu, kMaxSums);
+    const int64_t rounds = (units + fill - 1) / fill;
+    return rounds > 1 ? (int)((units + rounds - 1) / rounds) : (int)units;
+}
+
+// MI355X, 4, 8 or 16 workgroups per compute unit: partials 8 (k = 2 of 8 x 10^8
+// elements 487, 491, 495 us; k = 8 1900, 1907, 1876; 16 int8 partials 1984,
+// 1936, 1944), lists of tensors 4 (1.4 GB 213, 222, 229 us; 4.2 GB 615, 622, 631).
+constexpr int kPartialsPerCu = 8;
+constexpr int kTensorsPerCu = 4;
+
+// Bytes that a norm call reads last and with ordinary loads, for the step or the
+// scaling that follows to find in the last-level cache: its size.  The norm and
+// the step after it, three sets of buffers in turn, with 0, 64, 128, 192 and 256 MB:
+// n = 3.1 x 10^7, k = 2 193, 188, 179, 175, 174 us; 6.3 x 10^7, k = 2 399, 369, 360,
+// 335, 334; GPT-2-small (249 MB of partials) 160, 161, 158, 155, 152.  The norm alone
+// loses 4-8 % where all of it is read so and nothing measurable on large shards.
+constexpr int64_t kKeepBytes = int64_t(256) << 20;
+
+// Units of `unit_bytes` at the beginning of each XCD's run that make them up.
+int64_t kept_units(int xcds, int64_t unit_bytes) { return kKeepBytes / xcds / unit_bytes; }
+
+// Tables of at least this many pieces (256 MB) are scaled under a cap of
+// kClipCap workgroups per compute unit (1.4 GB: 455 us against 464 without, 457,
+// 464, 467 with 4, 6, 8; 4.2 GB: 1352 against 1414, 1352, 1381, 1416); below, the
+// cap changes nothing (200 MB: 66 us with and without).
+constexpr int64_t kClipCapMinPieces = (int64_t(1) << 28) / kPieceBytes;
+constexpr int kClipCap = 5;
+
+FinishArgs finish_args(void *workspace, zs_clip *clip, const Rule &rule) {
+    return {(double *)((char *)workspace + kCounterBytes), (uint32_t *)workspace, clip, rule};
 }
 
 int norm_call(bool q8, const uint16_t *const *grads, const int8_t *const *qgrads,
@@ -415,13 +457,14 @@ int norm_call(bool q8, const uint16_t *const *grads, const int8_t *const *qgrads
     if (st != ZS_OK) return st;
     a.n = n;
     a.gscale = grad_scale;
-    a.sums = (double *)workspace;
-    const int blocks = fill_blocks(dev, (n + kThreads - 1) / kThreads);
-    if (blocks > 0) {
-        const hipError_t e = launch_grad_norm(k, q8, a, blocks, (hipStream_t)stream);
-        if (e != hipSuccess) return device_error(e);
-    }
-    const hipError_t e = launch_finish(a.sums, blocks, r, clip, (hipStream_t)stream);
+    a.fin = finish_args(workspace, clip, r);
+    a.xcds = n >= kXcdOrderMinElems ? g_dev[dev].xcds : 1;  // the step's order
+    const int64_t tile = norm_tile(k, q8);
+    a.kept = kept_units(a.xcds, tile * k * (q8 ? 1 : 2));
+    const int blocks = norm_blocks(dev, (n + tile - 1) / tile, kPartialsPerCu);
+    const hipError_t e = blocks > 0
+                             ? launch_grad_norm(k, q8, a, blocks, (hipStream_t)stream)
+                             : launch_finish(a.fin.sums, 0, r, clip, (hipStream_t)stream);
     return e == hipSuccess ? ZS_OK : device_error(e);
 }
 
@@ -600,6 +643,24 @@ int zs_shard_step_packed_bf16mv_sr(float *state, uint16_t *param_bf16,
     return validate_and_launch(r);
 }
 
+int zs_shard_step_clipped(int variant, const zs_step_buffers *buffers, int k, int64_t n,
+                          const zs_seg_table *seg_table, const zs_hparams *hparams, int64_t step,
+                          uint64_t seed, const zs_clip *clip, void *stream) {
+    if (!buffers || !clip) return ZS_ERR_INVALID_ARGUMENT;
+    const zs_step_buffers &b = *buffers;
+    Request r = base_request(b.master, b.m, b.v, b.param_bf16, k, n, seg_table, hparams, step,
+                             stream);
+    r.q8 = b.param_q8;
+    r.q8_scale = b.param_q8_scale;
+    r.grads = b.grads;
+    r.qgrads = b.qgrads;
+    r.qscales = b.qscales;
+    r.variant = variant;
+    r.seed = seed;
+    r.clip = clip;
+    return validate_and_launch(r);
+}
+
 int zs_pack_state(const float *master, const float *m, const float *v, float *state, int64_t n,
                   void *stream) {
     return layout_call(kLayoutPack, false, const_cast<float *>(master), const_cast<float *>(m),
@@ -715,15 +776,13 @@ int zs_tensors_norm(const zs_tensor_table *table, const zs_clip_rule *rule, zs_c
     int dev = 0;
     st = current_device(&dev);
     if (st != ZS_OK) return st;
-    const int blocks =
-        fill_blocks(dev, (table->count + kThreads / kWave - 1) / (kThreads / kWave));
-    double *const sums = (double *)workspace;
-    if (blocks > 0) {
-        const hipError_t e = launch_tensors_norm(table->pieces, table->count, sums, blocks,
-                                                 (hipStream_t)stream);
-        if (e != hipSuccess) return device_error(e);
-    }
-    const hipError_t e = launch_finish(sums, blocks, r, clip, (hipStream_t)stream);
+    const FinishArgs fin = finish_args(workspace, clip, r);
+    const int blocks = norm_blocks(dev, (table->count + kGroup - 1) / kGroup, kTensorsPerCu);
+    const hipError_t e =
+        blocks > 0 ? launch_tensors_norm(table->pieces, table->count,
+                                         kept_units(1, kGroup * kPieceBytes), fin, blocks,
+                                         (hipStream_t)stream)
+                   : launch_finish(fin.sums, 0, r, clip, (hipStream_t)stream);
     return e == hipSuccess ? ZS_OK : device_error(e);
 }
 
@@ -735,11 +794,11 @@ int zs_tensors_clip(const zs_tensor_table *table, const zs_clip *clip, void *str
     int dev = 0;
     st = current_device(&dev);
     if (st != ZS_OK) return st;
-    const int blocks =
-        fill_blocks(dev, (table->count + kThreads / kWave - 1) / (kThreads / kWave));
-    if (blocks == 0) return ZS_OK;
-    const hipError_t e = launch_tensors_clip(table->pieces, table->count, clip, blocks,
-                                             (hipStream_t)stream);
+    if (table->count == 0) return ZS_OK;
+    const int64_t lds = table->count >= kClipCapMinPieces ? cap_lds(dev, kClipCap, 0) : 0;
+    const hipError_t e =
+        launch_tensors_clip(table->pieces, table->count, clip, std::min(table->count, kMaxBlocks),
+                            (size_t)std::max(lds, (int64_t)0), (hipStream_t)stream);
     return e == hipSuccess ? ZS_OK : device_error(e);
 }
 

@@ -109,6 +109,7 @@ struct StepArgs {
     int32_t xcds;   // XCDs the dispatcher deals workgroups to in turn; 1 = linear order
     float lr, b1, b2, c1, c2, bc1, bc2, eps, df, gscale;
     uint64_t sr_key_m, sr_key_v;  // kSR: the step's stream keys for m and v
+    const zs_clip *clip;  // DEVICE record of a clipped step, or null
 };
 
 constexpr int kQ8Block = ZS_Q8_BLOCK;
@@ -117,6 +118,41 @@ static_assert(kQ8Block == kSub, "a quantization block is one sub-window of a wav
 // LDS each workgroup of every kernel declares: one boundary slot per
 // wavefront, 64 eight-byte segment starts and 64 one-byte flags.
 constexpr int64_t kStaticLds = (int64_t)(8 + 1) * kWave * (kThreads / kWave);
+
+// ------------------------------------- device helpers of all the kernels
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t d) { return __uint_as_float(d << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t d) { return __uint_as_float(d & 0xffff0000u); }
+
+// Round to nearest even by adding 0x7fff plus the lowest kept bit, then
+// dropping 16 bits; NaN is mapped to the canonical quiet NaN.
+__device__ __forceinline__ uint32_t to_bf16(float x) {
+    const uint32_t u = __float_as_uint(x);
+    const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    return ((u & 0x7fffffffu) > 0x7f800000u) ? 0x7fc0u : r;
+}
+
+// Two values to packed bf16 with gfx950's v_cvt_pk_bf16_f32, which rounds to
+// nearest even and keeps denormals exactly as to_bf16 does but carries a NaN's
+// payload into the result; every NaN is therefore replaced by the canonical
+// quiet NaN first, which converts to 0x7FC0.
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+    const uint32_t qnan = 0x7fc00000u;
+    const f32x2 x = {__uint_as_float(__builtin_isnan(a) ? qnan : __float_as_uint(a)),
+                     __uint_as_float(__builtin_isnan(b) ? qnan : __float_as_uint(b))};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+}
+
+__device__ __forceinline__ float i8_at(uint32_t word, int byte) {
+    return (float)(int32_t)(int8_t)(uint8_t)(word >> (8 * byte));
+}
+
+// A clipping record as its readers see it, constant memory (scalar loads): the
+// norm call that wrote it was an earlier launch.
+typedef const __attribute__((address_space(4))) zs_clip ConstClip;
 
 typedef void (*kernel_fn)(const StepArgs);
 

@@ -49,8 +49,6 @@ namespace {
 constexpr int64_t kNoStart = INT64_MAX;       // sentinel past the table end
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <int NT, typename T>
@@ -63,17 +61,6 @@ template <int NT, typename T>
 __device__ __forceinline__ void store(T *p, T x) {
     if constexpr (NT) __builtin_nontemporal_store(x, p);
     else *p = x;
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t d) { return __uint_as_float(d << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t d) { return __uint_as_float(d & 0xffff0000u); }
-
-// Round to nearest even by adding 0x7fff plus the lowest kept bit, then
-// dropping 16 bits; NaN is mapped to the canonical quiet NaN.
-__device__ __forceinline__ uint32_t to_bf16(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-    return ((u & 0x7fffffffu) > 0x7f800000u) ? 0x7fc0u : r;
 }
 
 // One element of the update: g is the reduced, scaled gradient.  U1 (U2)
@@ -217,17 +204,6 @@ __device__ __forceinline__ f32x4 bf16x4_to_f32x4(u32x2 d) {
     return r;
 }
 
-// Two values to packed bf16 with gfx950's v_cvt_pk_bf16_f32, which rounds to
-// nearest even and keeps denormals exactly as to_bf16 does but carries a NaN's
-// payload into the result; every NaN is therefore replaced by the canonical
-// quiet NaN first, which converts to 0x7FC0.
-__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
-    const uint32_t qnan = 0x7fc00000u;
-    const f32x2 x = {__uint_as_float(__builtin_isnan(a) ? qnan : __float_as_uint(a)),
-                     __uint_as_float(__builtin_isnan(b) ? qnan : __float_as_uint(b))};
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
-}
-
 __device__ __forceinline__ u32x2 f32x4_to_bf16x4(f32x4 x) {
     u32x2 r;
     r[0] = pack_bf16x2(x[0], x[1]);
@@ -273,10 +249,6 @@ __device__ __forceinline__ uint32_t moment_bf16(float x, uint64_t key, int64_t i
     }
 }
 
-__device__ __forceinline__ float i8_at(uint32_t word, int byte) {
-    return (float)(int32_t)(int8_t)(uint8_t)(word >> (8 * byte));
-}
-
 // The four reduced gradients of one lane's quad (elements 4 * qi .. +3).
 template <int K, int V, int NT>
 struct QuadGrads {
@@ -300,7 +272,7 @@ struct QuadGrads {
     }
 
     // Left fold over the partials of element e (0..3 of the quad), then the scale.
-    __device__ __forceinline__ float reduced(int e, const StepArgs &a) const {
+    __device__ __forceinline__ float reduced(int e, float gscale) const {
 #pragma clang fp contract(off)
         float g;
         if constexpr (V & kGradQ8) {
@@ -316,13 +288,13 @@ struct QuadGrads {
 #pragma unroll
             for (int j = 1; j < K; ++j) g = g + ((e & 1) ? bf16_hi(bf[j][d]) : bf16_lo(bf[j][d]));
         }
-        return g * a.gscale;
+        return g * gscale;
     }
 };
 
 // Reduced gradient of one element in the scalar (ragged tail) path.
 template <int K, int V>
-__device__ __forceinline__ float scalar_grad(const StepArgs &a, int64_t i) {
+__device__ __forceinline__ float scalar_grad(const StepArgs &a, int64_t i, float gscale) {
 #pragma clang fp contract(off)
     float g;
     if constexpr (V & kGradQ8) {
@@ -338,7 +310,7 @@ __device__ __forceinline__ float scalar_grad(const StepArgs &a, int64_t i) {
 #pragma unroll
         for (int j = 1; j < K; ++j) g = g + __uint_as_float((uint32_t)a.grads[j][i] << 16);
     }
-    return g * a.gscale;
+    return g * gscale;
 }
 
 // Maximum over the 64 lanes of a wavefront (every lane gets it).
@@ -461,11 +433,11 @@ struct StateAt {
 // Reduce, update and pack one lane's quad.  mask bit e = decay of element e.
 template <int K, int V, int NT, bool U1, bool U2>
 __device__ __forceinline__ void quad_update(f32x4 &w, f32x4 &m, f32x4 &v,
-                                            const QuadGrads<K, V, NT> &gr, uint32_t mask,
-                                            const StepArgs &a, u32x2 &pout) {
+                                            const QuadGrads<K, V, NT> &gr, float gscale,
+                                            uint32_t mask, const StepArgs &a, u32x2 &pout) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float g = gr.reduced(e, a);
+        const float g = gr.reduced(e, gscale);
         float we = w[e], me = m[e], ve = v[e];
         adamw<U1, U2>(we, me, ve, g, (mask >> e) & 1u, a);
         w[e] = we;
@@ -497,6 +469,18 @@ __global__ __launch_bounds__(kThreads) void shard_step_kernel(const StepArgs a) 
         const int64_t nb = gridDim.x, q = nb / a.xcds, r = nb % a.xcds;
         const int64_t x = b % a.xcds, y = b / a.xcds;
         b = x * q + (x < r ? x : r) + y;
+    }
+    // The factor of the reduced gradient: a clipped step's coefficient comes
+    // from the device record, and a record that says so skips the step whole.
+    float gscale = a.gscale;
+    if (a.clip) {
+#pragma clang fp contract(off)
+        const ConstClip *const c = (const ConstClip *)a.clip;
+        if (!c->apply) return;
+        // one product per wave, back in a scalar register: a vector register more
+        // would cost the kernels of many partials a wave of occupancy
+        const float s = a.gscale * c->coef;
+        gscale = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(s)));
     }
     const int64_t c0 = b * a.chunk;
     const int64_t c1 = (c0 + a.chunk < a.n) ? c0 + a.chunk : a.n;
@@ -535,7 +519,7 @@ __global__ __launch_bounds__(kThreads) void shard_step_kernel(const StepArgs a) 
                 const int64_t qi = e[qd] / kQuad;
                 u32x2 pq;
                 quad_update<K, V, NT, (U & 1) != 0, (U & 2) != 0>(
-                    wv[qd], mv[qd], vv[qd], gq[qd], (mask >> (kQuad * qd)) & 0xfu, a, pq);
+                    wv[qd], mv[qd], vv[qd], gq[qd], gscale, (mask >> (kQuad * qd)) & 0xfu, a, pq);
                 const S st(a, e[qd]);
                 store<NT>(reinterpret_cast<f32x4 *>(st.w), wv[qd]);
                 S::template store_quad<NT>(st.m, mv[qd], a.sr_key_m, qi);
@@ -560,7 +544,7 @@ __global__ __launch_bounds__(kThreads) void shard_step_kernel(const StepArgs a) 
                 const int64_t i = e[q / kQuad] + (q % kQuad);
                 if (i >= a.n) continue;
                 valid |= 1u << q;
-                const float g = scalar_grad<K, V>(a, i);
+                const float g = scalar_grad<K, V>(a, i, gscale);
                 typedef StateAt<V> S;
                 const S st(a, i);
                 float wv = *st.w, mvv = S::load_one(st.m), vvv = S::load_one(st.v);

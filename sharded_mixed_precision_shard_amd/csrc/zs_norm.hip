@@ -5,9 +5,12 @@
 // Every element is squared and added in binary64.  The square of any fp32
 // value is a normal binary64 number, so no scaling is needed, and a sum of
 // 10^10 terms keeps about 6 decimal digits more than the fp32 result shows.
-// Each lane keeps one sum, a workgroup adds its lanes' in a fixed tree and
-// writes one value, and a second launch of one workgroup adds those: no
-// atomics, so the order is fixed.
+// Each lane keeps a few sums, a workgroup adds its lanes' in a fixed tree and
+// writes one value, and the workgroup that finishes last adds those in the
+// order of their indices: one launch, and an order that does not depend on
+// which workgroup is last.
+
+#include <type_traits>
 
 #include "zs_norm.h"
 
@@ -16,9 +19,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ float widen_bf16(uint16_t x) {
-    return __uint_as_float((uint32_t)x << 16);
-}
+__device__ __forceinline__ float widen_bf16(uint16_t x) { return bf16_lo(x); }
 
 __device__ __forceinline__ float widen_fp16(uint16_t x) {
     return (float)__builtin_bit_cast(_Float16, x);
@@ -33,13 +34,6 @@ __device__ __forceinline__ uint16_t round_fp16(float x) {
     return __builtin_bit_cast(uint16_t, (_Float16)x);
 }
 
-// fp32 to bf16, to nearest even: every NaN becomes 0x7FC0.
-__device__ __forceinline__ uint16_t round_bf16(float x) {
-    const uint32_t u = __float_as_uint(x);
-    const uint32_t r = (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
-    return (uint16_t)(((u & 0x7fffffffu) > 0x7f800000u) ? 0x7fc0u : r);
-}
-
 // Sum over a workgroup, in thread 0: a tree over each wavefront's lanes, then
 // the wavefronts in order.
 __device__ double workgroup_sum(double x) {
@@ -50,19 +44,77 @@ __device__ double workgroup_sum(double x) {
     double t = 0.0;
     if (threadIdx.x == 0)
         for (int w = 0; w < kThreads / kWave; ++w) t += s_wave[w];
+    __syncthreads();  // s_wave may be written again
     return t;
 }
 
-__device__ __forceinline__ float lo16(uint32_t d) { return __uint_as_float(d << 16); }
-__device__ __forceinline__ float hi16(uint32_t d) { return __uint_as_float(d & 0xffff0000u); }
-
-__device__ __forceinline__ float i8_at(uint32_t word, int byte) {
-    return (float)(int32_t)(int8_t)(uint8_t)(word >> (8 * byte));
+// The record of the sum S (one thread).
+__device__ void write_record(double s, const Rule &r, zs_clip *clip) {
+#pragma clang fp contract(off)
+    const double norm = sqrt(s);
+    const double d = norm + (double)r.eps;
+    const float f = (float)norm;
+    clip->sumsq = s;
+    clip->norm = f;
+    clip->coef = d <= (double)r.max_norm ? 1.0f : (float)((double)r.max_norm / d);
+    clip->apply = (r.skip_nonfinite && !__builtin_isfinite(f)) ? 0 : 1;
+    clip->reserved = 0;
 }
 
-template <typename T>
-__device__ __forceinline__ T load_once(const T *p) {
-    return __builtin_nontemporal_load(p);
+// One more arrival at a counter of `size`: whether it is the last, which sets
+// the counter back to 0.
+__device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t size) {
+    const uint32_t before =
+        __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (before != size - 1) return false;
+    __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
+// A norm call's end, for every workgroup: its sum goes to the workspace, and
+// the workgroup that arrives last adds all of them and writes the record.  No
+// workgroup waits for another.
+//
+// The workgroups sit on XCDs whose L2 caches do not see each other's writes,
+// so the sums are written and read by agent-scope atomics, which go past those
+// caches, and a workgroup arrives only when its own has been acknowledged (the
+// wait).  Acquire and release on the arrivals would say the same at the price
+// of an L2 write-back and an invalidation per workgroup, which no other data
+// here needs: an empty kernel of 2048 workgroups with one counter took 52 us
+// that way and 27 us this way.  The rest is the arrivals' taking turns at one
+// address, about 12 ns each, so a large grid arrives at kCounters counters and
+// their last arrivals at one more: 5.6 us, where the empty kernel alone takes
+// 1.7 and a second launch would add about 3.5 (and 2.5 us on the host).  Up to
+// kOneCounter workgroups one counter is faster (64: 3.0 against 3.2 us).
+__device__ void finish(double s, const FinishArgs &f) {
+    __shared__ int s_last;
+    s = workgroup_sum(s);
+    if (threadIdx.x == 0) {
+        __hip_atomic_store(f.sums + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint32_t n = gridDim.x, g = blockIdx.x % kCounters;
+        if (n <= kOneCounter)
+            s_last = last_of(f.counters, n);
+        else
+            s_last = last_of(f.counters + (1 + g) * kCounterStride,
+                             n / kCounters + (g < n % kCounters ? 1 : 0)) &&
+                     last_of(f.counters, kCounters);
+    }
+    __syncthreads();
+    if (!s_last) return;
+    double t = 0.0;
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kThreads)
+        t += __hip_atomic_load(f.sums + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    t = workgroup_sum(t);
+    if (threadIdx.x == 0) write_record(t, f.rule, f.clip);
+}
+
+// Keep: an ordinary load, which leaves the line in the last-level cache;
+// otherwise a streaming one, which does not displace what is there.
+template <bool Keep, typename T>
+__device__ __forceinline__ T load(const T *p) {
+    if constexpr (Keep) return *p;
+    else return __builtin_nontemporal_load(p);
 }
 
 // Four chains of additions per lane, so that they overlap.
@@ -80,20 +132,21 @@ struct PartialVectors {
     u32x4 d[K];
     float scale[Q8 ? K : 1];
 
+    template <bool Keep>
     __device__ __forceinline__ void load_from(const NormArgs &a, int64_t v) {
 #pragma unroll
         for (int j = 0; j < K; ++j) {
             if constexpr (Q8) {
-                d[j] = load_once(reinterpret_cast<const u32x4 *>(a.qgrads[j]) + v);
+                d[j] = load<Keep>(reinterpret_cast<const u32x4 *>(a.qgrads[j]) + v);
                 scale[j] = a.qscales[j][v * kElems / kQ8Block];
             } else {
-                d[j] = load_once(reinterpret_cast<const u32x4 *>(a.grads[j]) + v);
+                d[j] = load<Keep>(reinterpret_cast<const u32x4 *>(a.grads[j]) + v);
             }
         }
     }
     __device__ __forceinline__ float value(int j, int e) const {
         if constexpr (Q8) return i8_at(d[j][e / 4], e % 4) * scale[j];
-        else return (e & 1) ? hi16(d[j][e / 2]) : lo16(d[j][e / 2]);
+        else return (e & 1) ? bf16_hi(d[j][e / 2]) : bf16_lo(d[j][e / 2]);
     }
     // Left fold over the partials, then the scale, as the step forms it.
     __device__ __forceinline__ void add_squares(double (&s)[kChains], float gscale) const {
@@ -123,40 +176,66 @@ __device__ __forceinline__ float reduced(const NormArgs &a, int64_t i) {
     return g * a.gscale;
 }
 
-// Vectors a lane has in flight: about eight 16-byte loads.
-template <int K>
-constexpr int unroll_for() {
-    return K >= 8 ? 1 : 8 / K;
+// The units begin + y, begin + y + stride, ... below `end` that this workgroup
+// takes of `count`.  One XCD: every (grid size)-th unit.  More: the dispatcher
+// deals workgroup b to XCD b % xcds, and each XCD is given one contiguous run
+// of the units, which its workgroups take in turn, so that each L2 reads a
+// stream of its own.
+struct Share {
+    int64_t begin, end, stride, y;
+};
+
+__device__ __forceinline__ Share share_of(int64_t count, int xcds) {
+    if (xcds <= 1) return {0, count, (int64_t)gridDim.x, (int64_t)blockIdx.x};
+    const int64_t x = blockIdx.x % xcds, y = blockIdx.x / xcds;
+    const int64_t q = count / xcds, r = count % xcds;
+    const int64_t begin = x * q + (x < r ? x : r);
+    const int64_t groups = gridDim.x / xcds + (x < gridDim.x % xcds ? 1 : 0);
+    return {begin, begin + q + (x < r ? 1 : 0), groups, y};
+}
+
+// f(unit, keep) for the units of a share from the last to the first, keep being
+// true_type for the last `kept` of them to be read, those at the run's beginning.
+// What reads the data next (the step, the scaling) starts there and finds them
+// in the last-level cache.
+template <typename F>
+__device__ __forceinline__ void each_backwards(const Share &s, int64_t kept, F f) {
+    const int64_t mid = s.begin + kept < s.end ? s.begin + kept : s.end;
+    int64_t t = s.end - 1 - s.y;
+    for (; t >= mid; t -= s.stride) f(t, std::false_type());
+    for (; t >= s.begin; t -= s.stride) f(t, std::true_type());
 }
 
 template <int K, bool Q8>
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const NormArgs a) {
     typedef PartialVectors<K, Q8> Vec;
-    constexpr int U = unroll_for<K>();
+    constexpr int U = norm_unroll(K);
+    constexpr int kTileVectors = kThreads * U;
+    static_assert(kTileVectors * Vec::kElems == norm_tile(K, Q8), "the grid counts these tiles");
     const int64_t nv = a.n / Vec::kElems;  // whole vectors
-    const int64_t step = (int64_t)gridDim.x * kThreads * U;
+    const Share share = share_of((nv + kTileVectors - 1) / kTileVectors, a.xcds);
     double s[kChains] = {};
-    for (int64_t v0 = (int64_t)blockIdx.x * kThreads * U; v0 < nv; v0 += step) {
-        const int64_t v = v0 + threadIdx.x;
+    each_backwards(share, a.kept, [&](int64_t t, auto keep) {
+        constexpr bool kKeep = decltype(keep)::value;
+        const int64_t v = t * kTileVectors + threadIdx.x;
         Vec x[U];
-        if (v0 + kThreads * U <= nv) {
+        if ((t + 1) * kTileVectors <= nv) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) x[u].load_from(a, v + u * kThreads);
+            for (int u = 0; u < U; ++u) x[u].template load_from<kKeep>(a, v + u * kThreads);
 #pragma unroll
             for (int u = 0; u < U; ++u) x[u].add_squares(s, a.gscale);
         } else {
             for (int u = 0; u < U; ++u)
                 if (v + u * kThreads < nv) {
-                    x[0].load_from(a, v + u * kThreads);
+                    x[0].template load_from<kKeep>(a, v + u * kThreads);
                     x[0].add_squares(s, a.gscale);
                 }
         }
-    }
+    });
     // the elements past the last whole vector
     const int64_t i = nv * Vec::kElems + threadIdx.x;
     if (blockIdx.x == 0 && i < a.n) add_square(s[0], reduced<K, Q8>(a, i));
-    const double sum = workgroup_sum((s[0] + s[1]) + (s[2] + s[3]));
-    if (threadIdx.x == 0) a.sums[blockIdx.x] = sum;
+    finish((s[0] + s[1]) + (s[2] + s[3]), a.fin);
 }
 
 // --------------------------------------------------------------- tensor lists
@@ -185,7 +264,7 @@ __device__ __forceinline__ void piece_store(const zs_piece &p, uint32_t i, float
         return;
     }
     reinterpret_cast<uint16_t *>(p.addr)[i] =
-        p.dtype == ZS_DTYPE_BF16 ? round_bf16(x) : round_fp16(x);
+        p.dtype == ZS_DTYPE_BF16 ? (uint16_t)to_bf16(x) : round_fp16(x);
 }
 
 // A 16-byte vector of a type: elements, widening, and rounding back.
@@ -194,7 +273,7 @@ struct Vec16 {
     static constexpr int kElems = 16 / dtype_size(D);
     __device__ __forceinline__ static float get(const u32x4 &d, int e) {
         if constexpr (D == ZS_DTYPE_FP32) return __uint_as_float(d[e]);
-        else if constexpr (D == ZS_DTYPE_BF16) return (e & 1) ? hi16(d[e / 2]) : lo16(d[e / 2]);
+        else if constexpr (D == ZS_DTYPE_BF16) return (e & 1) ? bf16_hi(d[e / 2]) : bf16_lo(d[e / 2]);
         else return widen_fp16((uint16_t)(d[e / 2] >> (16 * (e & 1))));
     }
     __device__ __forceinline__ static void add_squares(double (&s)[kChains], const u32x4 &d) {
@@ -208,8 +287,7 @@ struct Vec16 {
             if constexpr (D == ZS_DTYPE_FP32) {
                 r[q] = __float_as_uint(__uint_as_float(d[q]) * c);
             } else if constexpr (D == ZS_DTYPE_BF16) {
-                r[q] = (uint32_t)round_bf16(lo16(d[q]) * c) |
-                       ((uint32_t)round_bf16(hi16(d[q]) * c) << 16);
+                r[q] = pack_bf16x2(bf16_lo(d[q]) * c, bf16_hi(d[q]) * c);
             } else {
                 r[q] = (uint32_t)round_fp16(get(d, 2 * q) * c) |
                        ((uint32_t)round_fp16(get(d, 2 * q + 1) * c) << 16);
@@ -238,100 +316,79 @@ __device__ __forceinline__ bool whole(const zs_piece &p) {
     return p.n * dtype_size(p.dtype) == kPieceBytes;  // starts at a multiple of kPieceBytes, too
 }
 
-template <uint32_t D>
+template <uint32_t D, bool Keep>
 __device__ __forceinline__ void norm_piece(const zs_piece &p, int lane, double (&s)[kChains]) {
     if (whole(p)) {
         const u32x4 *const v = reinterpret_cast<const u32x4 *>(p.addr) + lane;
         u32x4 d[kLaneVectors];
 #pragma unroll
-        for (int u = 0; u < kLaneVectors; ++u) d[u] = load_once(v + u * kWave);
+        for (int u = 0; u < kLaneVectors; ++u) d[u] = load<Keep>(v + u * kWave);
 #pragma unroll
         for (int u = 0; u < kLaneVectors; ++u) Vec16<D>::add_squares(s, d[u]);
         return;
     }
     const Split sp = split_of(p);
     const u32x4 *const v = reinterpret_cast<const u32x4 *>(p.addr + sp.head * dtype_size(D));
-    for (uint32_t u = lane; u < sp.vectors; u += kWave) Vec16<D>::add_squares(s, load_once(v + u));
+    for (uint32_t u = lane; u < sp.vectors; u += kWave) Vec16<D>::add_squares(s, v[u]);
     if ((uint32_t)lane < sp.head) add_square(s[0], piece_value(p, lane));
     if (sp.tail + lane < p.n) add_square(s[0], piece_value(p, sp.tail + lane));
 }
 
-// A wavefront takes every (waves in the grid)-th piece; the next one's
-// descriptor is loaded while this one's data is on its way.
-template <typename F>
-__device__ __forceinline__ void each_piece(const zs_piece *pieces, int64_t count, F f) {
-    const int64_t waves = (int64_t)gridDim.x * (kThreads / kWave);
-    int64_t b = (int64_t)blockIdx.x * (kThreads / kWave) +
-                __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (b >= count) return;
-    zs_piece p = piece_at(pieces, b);
-    while (true) {
-        const int64_t next = b + waves;
-        const zs_piece q = piece_at(pieces, next < count ? next : b);
-        f(p);
-        if (next >= count) return;
-        b = next;
-        p = q;
-    }
-}
-
+// A workgroup's share is of groups of kGroup consecutive pieces, one piece for
+// each of its wavefronts.
 __global__ __launch_bounds__(kThreads) void tensors_norm_kernel(const zs_piece *pieces,
-                                                                int64_t count, double *sums) {
+                                                                int64_t count, int64_t kept,
+                                                                FinishArgs fin) {
     const int lane = threadIdx.x % kWave;
     double s[kChains] = {};
-    each_piece(pieces, count, [&](const zs_piece &p) {
-        if (p.dtype == ZS_DTYPE_BF16) norm_piece<ZS_DTYPE_BF16>(p, lane, s);
-        else if (p.dtype == ZS_DTYPE_FP16) norm_piece<ZS_DTYPE_FP16>(p, lane, s);
-        else norm_piece<ZS_DTYPE_FP32>(p, lane, s);
+    each_backwards(share_of((count + kGroup - 1) / kGroup, 1), kept, [&](int64_t t, auto keep) {
+        constexpr bool kKeep = decltype(keep)::value;
+        const int64_t b = t * kGroup + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        if (b >= count) return;
+        const zs_piece p = piece_at(pieces, b);
+        if (p.dtype == ZS_DTYPE_BF16) norm_piece<ZS_DTYPE_BF16, kKeep>(p, lane, s);
+        else if (p.dtype == ZS_DTYPE_FP16) norm_piece<ZS_DTYPE_FP16, kKeep>(p, lane, s);
+        else norm_piece<ZS_DTYPE_FP32, kKeep>(p, lane, s);
     });
-    const double sum = workgroup_sum((s[0] + s[1]) + (s[2] + s[3]));
-    if (threadIdx.x == 0) sums[blockIdx.x] = sum;
+    finish((s[0] + s[1]) + (s[2] + s[3]), fin);
 }
 
+// One piece, by a whole workgroup: two vectors per lane.
 template <uint32_t D>
-__device__ __forceinline__ void clip_piece(const zs_piece &p, int lane, float coef) {
+__device__ __forceinline__ void clip_piece(const zs_piece &p, float coef) {
+    const uint32_t tid = threadIdx.x;
     if (whole(p)) {
-        u32x4 *const v = reinterpret_cast<u32x4 *>(p.addr) + lane;
-        u32x4 d[kLaneVectors];
+        u32x4 *const v = reinterpret_cast<u32x4 *>(p.addr) + tid;
+        constexpr int kEach = kPieceVectors / kThreads;
+        u32x4 d[kEach];
 #pragma unroll
-        for (int u = 0; u < kLaneVectors; ++u) d[u] = load_once(v + u * kWave);
+        for (int u = 0; u < kEach; ++u) d[u] = load<false>(v + u * kThreads);
 #pragma unroll
-        for (int u = 0; u < kLaneVectors; ++u)
-            __builtin_nontemporal_store(Vec16<D>::scaled(d[u], coef), v + u * kWave);
+        for (int u = 0; u < kEach; ++u)
+            __builtin_nontemporal_store(Vec16<D>::scaled(d[u], coef), v + u * kThreads);
         return;
     }
     const Split sp = split_of(p);
     u32x4 *const v = reinterpret_cast<u32x4 *>(p.addr + sp.head * dtype_size(D));
-    for (uint32_t u = lane; u < sp.vectors; u += kWave) v[u] = Vec16<D>::scaled(v[u], coef);
-    if ((uint32_t)lane < sp.head) piece_store(p, lane, piece_value(p, lane) * coef);
-    if (sp.tail + lane < p.n)
-        piece_store(p, sp.tail + lane, piece_value(p, sp.tail + lane) * coef);
+    for (uint32_t u = tid; u < sp.vectors; u += kThreads) v[u] = Vec16<D>::scaled(v[u], coef);
+    if (tid < sp.head) piece_store(p, tid, piece_value(p, tid) * coef);
+    if (sp.tail + tid < p.n) piece_store(p, sp.tail + tid, piece_value(p, sp.tail + tid) * coef);
 }
 
+// A workgroup takes one piece (more only where the grid cannot describe them
+// all).
 __global__ __launch_bounds__(kThreads) void tensors_clip_kernel(const zs_piece *pieces,
                                                                 int64_t count,
                                                                 const zs_clip *clip) {
-    const float coef = clip->coef;
-    if (!clip->apply || coef == 1.0f) return;
-    const int lane = threadIdx.x % kWave;
-    each_piece(pieces, count, [&](const zs_piece &p) {
-        if (p.dtype == ZS_DTYPE_BF16) clip_piece<ZS_DTYPE_BF16>(p, lane, coef);
-        else if (p.dtype == ZS_DTYPE_FP16) clip_piece<ZS_DTYPE_FP16>(p, lane, coef);
-        else clip_piece<ZS_DTYPE_FP32>(p, lane, coef);
-    });
-}
-
-// The record of the sum S (one thread).
-__device__ void write_record(double s, const Rule &r, zs_clip *clip) {
-#pragma clang fp contract(off)
-    const double norm = sqrt(s);
-    const double d = norm + (double)r.eps;
-    const float f = (float)norm;
-    clip->sumsq = s;
-    clip->norm = f;
-    clip->coef = d <= (double)r.max_norm ? 1.0f : (float)((double)r.max_norm / d);
-    clip->apply = (r.skip_nonfinite && !__builtin_isfinite(f)) ? 0 : 1;
-    clip->reserved = 0;
+    const ConstClip *const c = (const ConstClip *)clip;
+    const float coef = c->coef;
+    if (!c->apply || coef == 1.0f) return;
+    for (int64_t b = blockIdx.x; b < count; b += gridDim.x) {
+        const zs_piece p = piece_at(pieces, b);
+        if (p.dtype == ZS_DTYPE_BF16) clip_piece<ZS_DTYPE_BF16>(p, coef);
+        else if (p.dtype == ZS_DTYPE_FP16) clip_piece<ZS_DTYPE_FP16>(p, coef);
+        else clip_piece<ZS_DTYPE_FP32>(p, coef);
+    }
 }
 
 __global__ __launch_bounds__(kThreads) void finish_kernel(const double *sums, int count, Rule rule,
@@ -375,18 +432,19 @@ hipError_t launch_grad_norm(int k, bool q8, const NormArgs &a, int blocks, hipSt
     return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(kThreads), argv, 0, stream);
 }
 
-hipError_t launch_tensors_norm(const zs_piece *pieces, int64_t count, double *sums, int blocks,
-                               hipStream_t stream) {
-    void *argv[] = {&pieces, &count, &sums};
+hipError_t launch_tensors_norm(const zs_piece *pieces, int64_t count, int64_t kept,
+                               const FinishArgs &fin, int blocks, hipStream_t stream) {
+    FinishArgs f = fin;
+    void *argv[] = {&pieces, &count, &kept, &f};
     return hipLaunchKernel((const void *)tensors_norm_kernel, dim3((unsigned)blocks),
                            dim3(kThreads), argv, 0, stream);
 }
 
 hipError_t launch_tensors_clip(const zs_piece *pieces, int64_t count, const zs_clip *clip,
-                               int blocks, hipStream_t stream) {
+                               int64_t blocks, size_t lds, hipStream_t stream) {
     void *argv[] = {&pieces, &count, &clip};
     return hipLaunchKernel((const void *)tensors_clip_kernel, dim3((unsigned)blocks),
-                           dim3(kThreads), argv, 0, stream);
+                           dim3(kThreads), argv, lds, stream);
 }
 
 hipError_t launch_finish(const double *sums, int count, const Rule &rule, zs_clip *clip,

@@ -196,6 +196,57 @@ def test_elements_past_32_bits(gpu):
     check(rec, s, math.sqrt(s), 2.0 / math.sqrt(s))
 
 
+@pytest.mark.parametrize("k,form", [(1, "bf16"), (2, "bf16"), (3, "bf16"), (8, "bf16"),
+                                    (1, "int8"), (2, "int8"), (9, "int8")])
+def test_every_element_of_a_large_shard_counts_once(gpu, k, form):
+    """Shards on both sides of 2^26 elements, where the order of the work changes,
+    with ragged numbers of tiles: all ones, so that S = n k^2 exactly."""
+    torch = gpu
+    top = (1 << 26) + 8 * 70001 + 5
+    if form == "int8":
+        parts = [torch.ones(top, dtype=torch.int8, device="cuda")] * k
+        scales = [torch.ones(-(-top // 256), device="cuda")] * k
+    else:
+        parts, scales = [torch.ones(top, dtype=torch.bfloat16, device="cuda")] * k, None
+    for n in (1 << 24, (1 << 26) - 1, 1 << 26, (1 << 26) + 1, (1 << 26) + 4097, top):
+        rec = norm_of(torch, parts, n, None, 1.0, scales)
+        assert rec.sumsq.item() == float(n * k * k), n
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
+def test_every_element_of_a_large_list_counts_and_is_scaled_once(gpu, dtype):
+    torch = gpu
+    sizes = [60_000_001, 1, 8191, 70_000_003, 3, 4096, 20_000_000]
+    flat = torch.ones(sum(sizes), dtype=getattr(torch, dtype), device="cuda")
+    table, rec = zs.TensorTable(flat.split(sizes)), zs.ClipRecord()
+    zs.TensorsNorm(table, zs.clip_rule(0.5 * math.sqrt(sum(sizes)), 0.0), rec)()
+    assert rec.sumsq.item() == float(sum(sizes)) and abs(rec.coef.item() - 0.5) <= 2.0 ** -25
+    zs.zs_tensors_clip(table, rec)
+    assert bool((flat == (torch.ones(1) * rec.coef.cpu()).to(flat.dtype).cuda()).all())
+
+
+def test_many_calls_on_one_workspace(gpu):
+    """The arrival counters are back at 0 after every call: grids of one, a few,
+    tens, hundreds and a thousand workgroups in turn on one workspace."""
+    torch = gpu
+    rng = np.random.default_rng(77)
+    ws = zs.norm_workspace()
+    calls = []
+    for n in (5, 9000, 300_000, 40_000, 4_000_000, 2_000, 16_000_000, 140_000):
+        b = bf16_bits(np.ones(n) * float(rng.integers(1, 9)))
+        rec = zs.ClipRecord()
+        calls.append((zs.GradNorm([on_gpu(torch, b)], n, None, rec, workspace=ws), rec,
+                      n * float(widen(b)[0]) ** 2))
+    for rep in range(40):
+        for j in rng.permutation(len(calls)):
+            calls[j][0]()
+        torch.cuda.synchronize()
+        for _, rec, s in calls:
+            assert rec.sumsq.item() == s
+            rec.buffer.zero_()
+    assert not ws[:64].any()
+
+
 def test_same_call_same_bits(gpu):
     torch, n = gpu, 5_000_011
     rng = np.random.default_rng(5)
