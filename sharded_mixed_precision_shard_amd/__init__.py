@@ -809,6 +809,8 @@ class ClipRecord:
         self.norm = self.buffer[8:12].view(torch.float32)
         self.coef = self.buffer[12:16].view(torch.float32)
         self.apply = self.buffer[16:20].view(torch.int32)
+        self.device = self.buffer.device
+        self.address = _dev(self.buffer, ctypes.sizeof(ZsClip), "clip")
 
 
 def norm_workspace(device="cuda"):
@@ -818,8 +820,8 @@ def norm_workspace(device="cuda"):
 
 
 def _record(clip) -> int:
-    return _dev(clip.buffer if isinstance(clip, ClipRecord) else clip, ctypes.sizeof(ZsClip),
-                "clip")
+    return clip.address if isinstance(clip, ClipRecord) else _dev(clip, ctypes.sizeof(ZsClip),
+                                                                  "clip")
 
 
 def _rule(rule):
@@ -830,21 +832,28 @@ def _rule(rule):
 
 
 def _same_device(xs):
-    """The device index the given tensors share (None if none of them says)."""
-    devices = [getattr(x.buffer if isinstance(x, ClipRecord) else x, "device", None) for x in xs]
-    found = {d.index for d in devices if isinstance(getattr(d, "index", None), int)}
+    """The device index the given buffers share (None if none of them says)."""
+    found = {d.index for d in (getattr(x, "device", None) for x in xs)
+             if isinstance(getattr(d, "index", None), int)}
     if len(found) > 1:
         raise ValueError("buffers on different devices: %s" % sorted(found))
     return found.pop() if found else None
 
 
+_current_device = None
+
+
 def _on_device(index):
     """Refuse a call on buffers of a device that is not the current one."""
-    if index is not None:
+    global _current_device
+    if index is None:
+        return
+    if _current_device is None:
         import torch
-        if torch.cuda.current_device() != index:
-            raise ValueError("the buffers are on device %d, the current device is %d"
-                             % (index, torch.cuda.current_device()))
+        _current_device = torch.cuda.current_device
+    if _current_device() != index:
+        raise ValueError("the buffers are on device %d, the current device is %d"
+                         % (index, _current_device()))
 
 
 class GradNorm:
@@ -964,12 +973,12 @@ class TensorTable:
         import torch
         tensors = list(tensors)
         pieces = zs_tensor_pieces(tensors)
-        self.device = _same_device(tensors)
+        index = _same_device(tensors)
+        self.device = None if index is None else torch.device("cuda", index)
         self.tensors = tensors
         self.buffer = None
         if len(pieces):
-            host = torch.frombuffer(pieces, dtype=torch.uint8)
-            self.buffer = host.to(torch.device("cuda", self.device))
+            self.buffer = torch.frombuffer(pieces, dtype=torch.uint8).to(self.device)
         self.table = ZsTensorTable(_dev(self.buffer, ctypes.sizeof(pieces), "pieces"), len(pieces))
 
 
@@ -978,7 +987,7 @@ class TensorsNorm:
     its own unless one is given."""
 
     def __init__(self, table, rule, clip, workspace=None):
-        self._device = _same_device([clip, workspace, *table.tensors[:1]])
+        self._device = _same_device([clip, workspace, table])
         if workspace is None:
             workspace = norm_workspace("cuda" if self._device is None else self._device)
         self._keep = [table, rule, clip, workspace]
@@ -1001,7 +1010,7 @@ def zs_tensors_norm(table, rule, clip, workspace, stream=None, check=True) -> in
 
 def zs_tensors_clip(table, clip, stream=None, check=True) -> int:
     """Enqueue the scaling of a TensorTable's tensors by the record's coef, in place."""
-    _on_device(_same_device([clip, *table.tensors[:1]]))
+    _on_device(_same_device([clip, table]))
     rc = load_library().zs_tensors_clip(ctypes.byref(table.table), _record(clip),
                                         _stream_handle(stream))
     if check and rc != ZS_OK:
