@@ -33,6 +33,10 @@
  * the 16 dropped bits; every NaN becomes 0x7FC0.  "AdamW" decay is read as
  * decoupled and lr-coupled, applied to the pre-step weight.
  *
+ * Beside the step: the norm of the gradient over all parameters, clipping by
+ * it, and the step on the clipped gradient ("Global gradient norm and
+ * clipping" below).
+ *
  * Threading: zs_init/zs_fini must not race with other calls.  After
  * zs_init the library holds no mutable state, so zs_shard_step may be
  * called concurrently from several threads and on several streams.
