@@ -384,6 +384,10 @@ int zs_unpack_state_bf16mv(const float *state, float *master, uint16_t *m_bf16, 
  * sumsq field, or an all-gather) and zs_clip_combine forms norm and coef of
  * the total.
  *
+ * Each of these calls enqueues one kernel and nothing else, so they may be
+ * recorded into a HIP graph, as the step may.  What one call writes into a
+ * record another reads in stream order; across streams the caller orders them.
+ *
  * Numerics: each element is squared and summed in binary64, where no square
  * of an fp32 value overflows or vanishes; norm and coef are formed in binary64
  * and rounded once to binary32.  The order of the sum is fixed by the sizes

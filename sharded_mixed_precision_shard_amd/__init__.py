@@ -795,6 +795,16 @@ def clip_rule(max_norm, eps=1e-6, skip_nonfinite=False) -> ZsClipRule:
     return ZsClipRule(max_norm, eps, 1 if skip_nonfinite else 0, 0)
 
 
+def _zeroed(nbytes, device):
+    """Zeroed device memory that any stream may use at once: the fill is waited
+    for (in a graph being captured it is a node of the graph instead)."""
+    import torch
+    buffer = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    if buffer.is_cuda and not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(buffer.device).synchronize()
+    return buffer
+
+
 class ClipRecord:
     """A device record (zs_clip) that a norm call writes and a clipped step or
     zs_tensors_clip reads: one-element views ``sumsq`` (float64), ``norm``,
@@ -804,7 +814,7 @@ class ClipRecord:
 
     def __init__(self, device="cuda"):
         import torch
-        self.buffer = torch.zeros(ctypes.sizeof(ZsClip), dtype=torch.uint8, device=device)
+        self.buffer = _zeroed(ctypes.sizeof(ZsClip), device)
         self.sumsq = self.buffer[0:8].view(torch.float64)
         self.norm = self.buffer[8:12].view(torch.float32)
         self.coef = self.buffer[12:16].view(torch.float32)
@@ -815,8 +825,7 @@ class ClipRecord:
 
 def norm_workspace(device="cuda"):
     """Workspace of a norm call, zeroed; calls that may overlap in time need one each."""
-    import torch
-    return torch.zeros(ZS_NORM_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+    return _zeroed(ZS_NORM_WORKSPACE_BYTES, device)
 
 
 def _record(clip) -> int:
@@ -856,12 +865,21 @@ def _on_device(index):
                          % (index, _current_device()))
 
 
+def _check_type(xs, allowed, name):
+    """Refuse tensors whose dtype says that their bytes mean something else."""
+    for j, x in enumerate(xs):
+        dtype = str(getattr(x, "dtype", allowed[0]))
+        if dtype not in allowed:
+            raise TypeError("%s[%d] is %s, not %s" % (name, j, dtype, " or ".join(allowed)))
+
+
 class GradNorm:
     """The norm call on a shard's partials with its buffers fixed: checked and
     marshalled once, as ShardStep does for the step.  ``partials`` are bf16
     [n], or int8 [n] with their block scales ``qscales``; ``rule`` is a
-    clip_rule or None; ``clip`` the record it writes.  The workspace is its own
-    unless one is given."""
+    clip_rule or None, read at each call; ``clip`` the record it writes.  The
+    workspace is its own unless one is given, so keep the object until its
+    calls have run, and give calls on several streams an object each."""
 
     def __init__(self, partials, n, rule, clip, grad_scale=1.0, qscales=None, workspace=None):
         lib = load_library()
@@ -875,9 +893,12 @@ class GradNorm:
             workspace = norm_workspace("cuda" if self._device is None else self._device)
         self._keep = [list(partials), qscales, rule, clip, workspace]
         if qscales is None:
+            _check_type(partials, ("torch.bfloat16", "torch.int16", "torch.uint16"), "grads")
             self._c = (_ptr_array(partials, 2 * nn, "grads"),)
             self._fn, self._name = lib.zs_grad_norm, "zs_grad_norm"
         else:
+            _check_type(partials, ("torch.int8",), "qgrads")
+            _check_type(qscales, ("torch.float32",), "qscales")
             self._c = (_ptr_array(partials, nn, "qgrads"),
                        _ptr_array(qscales, 4 * -(-nn // ZS_Q8_BLOCK), "qscales"))
             self._fn, self._name = lib.zs_grad_norm_q8grad, "zs_grad_norm_q8grad"

@@ -496,15 +496,66 @@ def test_replayed_graphs_and_streams(gpu):
         check(r, *reference(fold([widen(b) for b in bs], 1.0), 1.0, float(np.float32(1e-6))))
 
 
+def test_objects_made_on_a_busy_stream_are_ready_on_another(gpu):
+    """Record, workspace and table are made while the current stream is busy, and
+    used at once on another stream."""
+    torch = gpu
+    side, n = torch.cuda.Stream(), 700_001
+    bits = partials(np.random.default_rng(8), n, 1)
+    part = on_gpu(torch, bits[0])
+    x = torch.ones(300_000, device="cuda")
+    garbage = torch.full((1 << 20,), 0x55, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    del garbage                            # what a new allocation may find in its memory
+    for rep in range(4):
+        torch.cuda._sleep(20_000_000)
+        rec, rec_x = zs.ClipRecord(), zs.ClipRecord()
+        norm = zs.GradNorm([part], n, zs.clip_rule(1.0), rec)
+        norm_x = zs.TensorsNorm(zs.TensorTable([x]), zs.clip_rule(1.0), rec_x)
+        norm(side)
+        norm_x(side)
+        side.synchronize()
+        check(rec, *reference(widen(bits[0]), 1.0, float(np.float32(1e-6))))
+        assert rec_x.sumsq.item() == 300_000.0
+    torch.cuda.synchronize()
+
+
+def test_objects_made_during_a_capture(gpu):
+    """Their zeroing becomes part of the graph: every replay starts from it."""
+    torch, n = gpu, 500_009
+    rng = np.random.default_rng(12)
+    part = on_gpu(torch, partials(rng, n, 1)[0])
+    norm_of(torch, [part], n)              # the kernel is loaded before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rec = zs.ClipRecord()
+        norm = zs.GradNorm([part], n, zs.clip_rule(1.0), rec)
+        norm(torch.cuda.current_stream())
+    for _ in range(4):
+        bits = partials(rng, n, 1)[0]
+        part[:n] = torch.from_numpy(bits.view(np.int16)).cuda()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check(rec, *reference(widen(bits), 1.0, float(np.float32(1e-6))))
+        assert torch.isfinite(torch.randn(4096, device="cuda").square().sum())
+        torch.cuda.synchronize()
+
+
 def test_errors_are_reported(gpu):
     rec, ws = zs.ClipRecord(), zs.norm_workspace()
     g = on_gpu(gpu, np.zeros(64, np.uint16))
     with pytest.raises(zs.ZsError, match="invalid argument"):
         zs.zs_grad_norm([g], 1, 64, math.nan, None, rec, ws)
+    with pytest.raises(TypeError, match=r"grads\[0\] is torch.float16"):
+        zs.zs_grad_norm([g.view(gpu.float16)], 1, 64, 1.0, None, rec, ws)
+    with pytest.raises(TypeError, match=r"qscales\[0\] is torch.int32"):
+        zs.zs_grad_norm_q8grad([g.view(gpu.int8)], [g.view(gpu.int32)], 1, 64, 1.0, None, rec, ws)
     with pytest.raises(zs.ZsError, match="not aligned"):
         zs.zs_grad_norm([g[1:]], 1, 8, 1.0, None, rec, ws)
     with pytest.raises(zs.ZsError, match="overlap"):
-        zs.zs_grad_norm([ws], 1, 64, 1.0, None, rec, ws)
+        zs.zs_grad_norm([ws.view(gpu.int16)], 1, 64, 1.0, None, rec, ws)
     assert zs.zs_clip_combine(rec.sumsq, zs.clip_rule(-1.0), rec, check=False) == \
         zs.ZS_ERR_INVALID_ARGUMENT
     assert rec.apply.item() == 0     # nothing was enqueued
