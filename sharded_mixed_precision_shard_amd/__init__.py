@@ -20,6 +20,7 @@ Entry points keep the C names: :func:`zs_init`, :func:`zs_shard_step`,
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -842,11 +843,19 @@ def _rule(rule):
 
 def _same_device(xs):
     """The device index the given buffers share (None if none of them says)."""
-    found = {d.index for d in (getattr(x, "device", None) for x in xs)
-             if isinstance(getattr(d, "index", None), int)}
-    if len(found) > 1:
-        raise ValueError("buffers on different devices: %s" % sorted(found))
-    return found.pop() if found else None
+    found = None
+    for x in xs:
+        index = getattr(getattr(x, "device", None), "index", None)
+        if isinstance(index, int):
+            if found is not None and index != found:
+                raise ValueError("buffers on different devices: %s" % sorted((found, index)))
+            found = index
+    return found
+
+
+@functools.lru_cache(maxsize=None)
+def _type_name(dtype) -> str:
+    return str(dtype)
 
 
 _current_device = None
@@ -868,7 +877,7 @@ def _on_device(index):
 def _check_type(xs, allowed, name):
     """Refuse tensors whose dtype says that their bytes mean something else."""
     for j, x in enumerate(xs):
-        dtype = str(getattr(x, "dtype", allowed[0]))
+        dtype = _type_name(getattr(x, "dtype", allowed[0]))
         if dtype not in allowed:
             raise TypeError("%s[%d] is %s, not %s" % (name, j, dtype, " or ".join(allowed)))
 
@@ -931,7 +940,7 @@ def zs_clip_combine(sumsq, rule, clip, stream=None, count=None, check=True) -> i
     """Norm and coefficient of the sum of ``sumsq`` (device float64 [count]), for
     instance the ranks' gathered sums, or the record's own after an all-reduce."""
     if not isinstance(sumsq, int):
-        if str(getattr(sumsq, "dtype", "")) not in ("", "torch.float64"):
+        if _type_name(getattr(sumsq, "dtype", "torch.float64")) != "torch.float64":
             raise TypeError("sumsq must be float64, got %s" % sumsq.dtype)
         count = sumsq.numel() if count is None else count
     args = [_dev(sumsq, 8 * max(int(count), 0), "sumsq"), int(count), _rule(rule), _record(clip)]
@@ -966,11 +975,11 @@ def zs_tensor_pieces(tensors):
         name = "tensors[%d]" % i
         if not getattr(x, "is_cuda", False):
             raise ValueError("%s must be a GPU tensor" % name)
-        if str(x.dtype) not in ZS_DTYPE:
+        if _type_name(x.dtype) not in ZS_DTYPE:
             raise TypeError("%s: %s is not bfloat16, float16 or float32" % (name, x.dtype))
         if not _dense(x):
             raise ValueError("%s must be dense: its elements without gaps or repeats" % name)
-        arr[i].data, arr[i].n, arr[i].dtype = x.data_ptr(), x.numel(), ZS_DTYPE[str(x.dtype)]
+        arr[i].data, arr[i].n, arr[i].dtype = x.data_ptr(), x.numel(), ZS_DTYPE[_type_name(x.dtype)]
     lib = load_library()
     made = ctypes.c_int64(0)
     rc = lib.zs_tensor_pieces(arr, len(tensors), None, 0, ctypes.byref(made))
