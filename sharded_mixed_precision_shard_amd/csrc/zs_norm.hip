@@ -115,8 +115,8 @@ __device__ void finish(double s, const FinishArgs &f) {
 
 // Keep: an ordinary load, which leaves the line in the last-level cache;
 // otherwise a streaming one, which does not displace what is there.
-template <bool Keep, typename T>
-__device__ __forceinline__ T load(const T *p) {
+template <bool Keep, typename P>
+__device__ __forceinline__ u32x4 load(P p) {
     if constexpr (Keep) return *p;
     else return __builtin_nontemporal_load(p);
 }
@@ -261,18 +261,28 @@ __device__ __forceinline__ zs_piece piece_at(const zs_piece *pieces, int64_t b) 
     return {c->addr, c->n, c->dtype};
 }
 
+// An address from a descriptor as a pointer to global memory: the compiler
+// cannot tell by itself and would take flat loads and stores.
+template <typename T>
+using Global = __attribute__((address_space(1))) T;
+
+template <typename T>
+__device__ __forceinline__ Global<T> *global_at(uint64_t addr) {
+    return reinterpret_cast<Global<T> *>(addr);
+}
+
 __device__ __forceinline__ float piece_value(const zs_piece &p, uint32_t i) {
-    if (p.dtype == ZS_DTYPE_FP32) return reinterpret_cast<const float *>(p.addr)[i];
-    const uint16_t x = reinterpret_cast<const uint16_t *>(p.addr)[i];
+    if (p.dtype == ZS_DTYPE_FP32) return global_at<const float>(p.addr)[i];
+    const uint16_t x = global_at<const uint16_t>(p.addr)[i];
     return p.dtype == ZS_DTYPE_BF16 ? widen_bf16(x) : widen_fp16(x);
 }
 
 __device__ __forceinline__ void piece_store(const zs_piece &p, uint32_t i, float x) {
     if (p.dtype == ZS_DTYPE_FP32) {
-        reinterpret_cast<float *>(p.addr)[i] = x;
+        global_at<float>(p.addr)[i] = x;
         return;
     }
-    reinterpret_cast<uint16_t *>(p.addr)[i] =
+    global_at<uint16_t>(p.addr)[i] =
         p.dtype == ZS_DTYPE_BF16 ? (uint16_t)to_bf16(x) : round_fp16(x);
 }
 
@@ -328,7 +338,7 @@ __device__ __forceinline__ bool whole(const zs_piece &p) {
 template <uint32_t D, bool Keep>
 __device__ __forceinline__ void norm_piece(const zs_piece &p, int lane, double (&s)[kChains]) {
     if (whole(p)) {
-        const u32x4 *const v = reinterpret_cast<const u32x4 *>(p.addr) + lane;
+        const Global<u32x4> *const v = global_at<u32x4>(p.addr) + lane;
         u32x4 d[kLaneVectors];
 #pragma unroll
         for (int u = 0; u < kLaneVectors; ++u) d[u] = load<Keep>(v + u * kWave);
@@ -337,8 +347,8 @@ __device__ __forceinline__ void norm_piece(const zs_piece &p, int lane, double (
         return;
     }
     const Split sp = split_of(p);
-    const u32x4 *const v = reinterpret_cast<const u32x4 *>(p.addr + sp.head * dtype_size(D));
-    for (uint32_t u = lane; u < sp.vectors; u += kWave) Vec16<D>::add_squares(s, v[u]);
+    const Global<u32x4> *const v = global_at<u32x4>(p.addr + sp.head * dtype_size(D));
+    for (uint32_t u = lane; u < sp.vectors; u += kWave) Vec16<D>::add_squares(s, load<true>(v + u));
     if ((uint32_t)lane < sp.head) add_square(s[0], piece_value(p, lane));
     if (sp.tail + lane < p.n) add_square(s[0], piece_value(p, sp.tail + lane));
 }
@@ -367,7 +377,7 @@ template <uint32_t D>
 __device__ __forceinline__ void clip_piece(const zs_piece &p, float coef) {
     const uint32_t tid = threadIdx.x;
     if (whole(p)) {
-        u32x4 *const v = reinterpret_cast<u32x4 *>(p.addr) + tid;
+        Global<u32x4> *const v = global_at<u32x4>(p.addr) + tid;
         constexpr int kEach = kPieceVectors / kThreads;
         u32x4 d[kEach];
 #pragma unroll
@@ -378,8 +388,8 @@ __device__ __forceinline__ void clip_piece(const zs_piece &p, float coef) {
         return;
     }
     const Split sp = split_of(p);
-    u32x4 *const v = reinterpret_cast<u32x4 *>(p.addr + sp.head * dtype_size(D));
-    for (uint32_t u = tid; u < sp.vectors; u += kThreads) v[u] = Vec16<D>::scaled(v[u], coef);
+    Global<u32x4> *const v = global_at<u32x4>(p.addr + sp.head * dtype_size(D));
+    for (uint32_t u = tid; u < sp.vectors; u += kThreads) v[u] = Vec16<D>::scaled(load<true>(v + u), coef);
     if (tid < sp.head) piece_store(p, tid, piece_value(p, tid) * coef);
     if (sp.tail + tid < p.n) piece_store(p, sp.tail + tid, piece_value(p, sp.tail + tid) * coef);
 }

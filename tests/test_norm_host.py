@@ -200,6 +200,19 @@ def test_table_refusals():
     assert lib.zs_tensors_clip(table(), HOLE + 4, None) == MISALIGNED
 
 
+def test_clipped_step_refusals():
+    """The record and the buffers are looked at first, then what every step checks
+    (on this machine: that the library is initialized)."""
+    lib, hp = zs.load_library(), zs.hparams()
+    b, st = zs.ZsStepBuffers(), zs.ZsSegTable(4096, 1, 0)
+
+    def call(buffers=b, clip=HOLE):
+        return lib.zs_shard_step_clipped(0, ctypes.byref(buffers) if buffers else None, 1, 100,
+                                         ctypes.byref(st), ctypes.byref(hp), 1, 0, clip, None)
+    assert call() == NOT_INIT
+    assert call(buffers=None) == INVALID and call(clip=None) == INVALID
+
+
 class Tensor:
     """Answers what the binding asks of a GPU tensor, at an address never used."""
 
@@ -240,6 +253,35 @@ def test_binding_takes_dense_tensors_in_any_order():
     torch = pytest.importorskip("torch")
     with pytest.raises(ValueError, match="GPU tensor"):
         zs.zs_tensor_pieces([torch.zeros(4)])
+
+
+def test_binding_refusals_of_the_clipped_step():
+    n = 1000
+    f = [FakeGpuTensor(4 * n) for _ in range(3)] + [FakeGpuTensor(2 * n)]
+    g, st, hp, rec = [FakeGpuTensor(2 * n)], zs.seg_table(FakeGpuTensor(16), 1), zs.hparams(), \
+        FakeGpuTensor(24)
+    with pytest.raises(ValueError, match="needs a record"):
+        zs.zs_shard_step_clipped("base", *f, g, n, st, hp, 1, None)
+    with pytest.raises(ValueError, match="clip holds"):
+        zs.ShardStep(*f, g, n, st, hp, clip=FakeGpuTensor(16))
+    with pytest.raises(TypeError, match="host"):
+        zs.ShardStep(*f, g, n, st, hp, clip=np.zeros(24, np.uint8))
+    with pytest.raises(ValueError, match="no launch cfg"):
+        zs.ShardStep(*f, g, n, st, hp, cfg=dict(chunk_tiles=2), clip=rec)
+    with pytest.raises(ValueError, match="m holds"):
+        zs.zs_shard_step_clipped("base", f[0], FakeGpuTensor(2 * n), f[2], f[3], g, n, st, hp, 1, rec)
+    # every form takes exactly the buffers it names (null addresses: the library refuses)
+    nb = -(-n // 256)
+    more = dict(q8ag=dict(param_q8=FakeGpuTensor(n), param_q8_scale=FakeGpuTensor(4 * nb)),
+                q8grad=dict(qscales=[FakeGpuTensor(4 * nb)]))
+    for form in zs.ZS_VARIANT:
+        state = FakeGpuTensor(4 * zs.packed_floats(n))
+        head = (state, None, None, f[3]) if form.startswith("packed") else f
+        kw = {k: v for name, v in more.items() if form.endswith(name) for k, v in v.items()}
+        if form.endswith("_sr"):
+            kw["seed"] = 3
+        step = zs.ShardStep(*head, g, n, st, hp, variant=form, clip=rec, **kw)
+        assert step(1, check=False) in (NOT_INIT, INVALID)
 
 
 def test_binding_refusals():
