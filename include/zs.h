@@ -470,7 +470,9 @@ int zs_clip_combine(const double *sumsq, int count, const zs_clip_rule *rule, zs
  *   seed    : for the _SR variants, otherwise ignored
  *   clip    : DEVICE record, 8-byte aligned, apart from every output
  * Everything else, errors and HBM traffic as for the entry point; the record
- * is one more read per workgroup.  Capturing the norm call and the step into
+ * is one more read per workgroup.  The chunk order may be XCD-contiguous on
+ * smaller shards than zs_launch_plan reports for the entry point (the order
+ * its norm call reads in); results do not depend on it.  Capturing the norm call and the step into
  * one graph makes every replay clip by the norm of that replay's gradient.
  */
 typedef struct {

@@ -137,6 +137,27 @@ int resolve_launch(int k, int64_t n, int variant, const zs_launch_cfg *cfg,
     return ZS_OK;
 }
 
+// The order of a norm call and of the clipped step after it: XCD-contiguous for
+// shards that the step takes so anyway, and below them for partials of 8 bytes
+// per element (4 bf16, 8 int8) and 4 MB in all.  Both calls then read an element
+// on the same XCD, and what the norm read last is still in its L2 (32 MB over
+// the device) when the step starts there.  Norm and step, linear and
+// XCD-contiguous, three sets of buffers in turn: k = 4, n = 7 x 10^5 11.9 and
+// 10.9 us, 2^20 14.9 and 13.0, 2 x 10^7 134 and 129, 6 x 10^7 412 and 414; k = 8,
+// 1.3 x 10^6 20.2 and 18.4, 7.7 x 10^6 77.4 and 73.9; k = 16, 1.3 x 10^6 27.2 and 23.9;
+// the other forms alike.  With one or two bf16 partials it goes either way at
+// 10^6 elements (12.2 and 11.5 us, 11.9 and 11.7) and loses 2-5 % from 3 x 10^6 on,
+// with four int8 ones 2-4 % from 7 x 10^6 on; with 3 x 10^5 elements it gains
+// nothing up to k = 8.
+constexpr int kPairRunsMinPerElem = 8;
+constexpr int64_t kPairRunsMinBytes = int64_t(1) << 22;
+
+bool pair_runs(int k, int64_t n, bool q8) {
+    const int64_t per_elem = (q8 ? 1 : 2) * k;
+    return n >= kXcdOrderMinElems ||
+           (per_elem >= kPairRunsMinPerElem && per_elem * n >= kPairRunsMinBytes);
+}
+
 // One call, whatever the variant: the buffers it reads and writes.
 struct Request {
     float *master = nullptr;
@@ -291,7 +312,7 @@ int validate_and_launch(const Request &r) {
 
     const int64_t blocks = plan.workgroups;
     a.chunk = plan.chunk_elements;
-    a.xcds = plan.block_order == 2 ? g_dev[dev].xcds : 1;
+    a.xcds = plan.block_order == 2 || (r.clip && pair_runs(r.k, n, gq)) ? g_dev[dev].xcds : 1;
     const bool default_cap = plan.groups_per_cu < 0;
     const int groups_per_cu = default_cap ? -plan.groups_per_cu : plan.groups_per_cu;
 
@@ -458,7 +479,7 @@ int norm_call(bool q8, const uint16_t *const *grads, const int8_t *const *qgrads
     a.n = n;
     a.gscale = grad_scale;
     a.fin = finish_args(workspace, clip, r);
-    a.xcds = n >= kXcdOrderMinElems ? g_dev[dev].xcds : 1;  // the step's order
+    a.xcds = pair_runs(k, n, q8) ? g_dev[dev].xcds : 1;
     const int64_t tile = norm_tile(k, q8);
     a.kept = kept_units(a.xcds, tile * k * (q8 ? 1 : 2));
     const int blocks = norm_blocks(dev, (n + tile - 1) / tile, kPartialsPerCu);

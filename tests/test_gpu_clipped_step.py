@@ -84,7 +84,7 @@ def hp_of(grad_scale):
 
 
 @pytest.mark.parametrize("form", H.VARIANTS)
-@pytest.mark.parametrize("n,k", [(1, 1), (255, 2), (257, 3), (1000, 16), (100003, 4)])
+@pytest.mark.parametrize("n,k", [(1, 1), (255, 2), (257, 3), (1000, 16), (100003, 4), (600_011, 8)])
 def test_every_form_equals_the_unclipped_step_on_the_scaled_gradient(gpu, form, n, k):
     torch = gpu
     for t in (3, 200, 10000):        # all three kernels of the bias corrections

@@ -199,8 +199,8 @@ def test_elements_past_32_bits(gpu):
 @pytest.mark.parametrize("k,form", [(1, "bf16"), (2, "bf16"), (3, "bf16"), (8, "bf16"),
                                     (1, "int8"), (2, "int8"), (9, "int8")])
 def test_every_element_of_a_large_shard_counts_once(gpu, k, form):
-    """Shards on both sides of 2^26 elements, where the order of the work changes,
-    with ragged numbers of tiles: all ones, so that S = n k^2 exactly."""
+    """Shards on both sides of 2^26 elements and of 4 MB of partials, where the order
+    of the work changes, with ragged numbers of tiles: all ones, so that S = n k^2 exactly."""
     torch = gpu
     top = (1 << 26) + 8 * 70001 + 5
     if form == "int8":
@@ -208,7 +208,8 @@ def test_every_element_of_a_large_shard_counts_once(gpu, k, form):
         scales = [torch.ones(-(-top // 256), device="cuda")] * k
     else:
         parts, scales = [torch.ones(top, dtype=torch.bfloat16, device="cuda")] * k, None
-    for n in (1 << 24, (1 << 26) - 1, 1 << 26, (1 << 26) + 1, (1 << 26) + 4097, top):
+    for n in (1 << 18, (1 << 19) - 1, 1 << 19, 524_289 + 777, 1 << 24, (1 << 26) - 1, 1 << 26,
+              (1 << 26) + 1, (1 << 26) + 4097, top):
         rec = norm_of(torch, parts, n, None, 1.0, scales)
         assert rec.sumsq.item() == float(n * k * k), n
 
