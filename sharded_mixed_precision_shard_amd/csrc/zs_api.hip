@@ -413,11 +413,14 @@ int norm_blocks(int dev, int64_t units, int per_cu) {
     return rounds > 1 ? (int)((units + rounds - 1) / rounds) : (int)units;
 }
 
-// MI355X, 4, 8 or 16 workgroups per compute unit: partials 8 (k = 2 of 8 x 10^8
-// elements 487, 491, 495 us; k = 8 1900, 1907, 1876; 16 int8 partials 1984,
-// 1936, 1944), lists of tensors 4 (1.4 GB 213, 222, 229 us; 4.2 GB 615, 622, 631).
-constexpr int kPartialsPerCu = 8;
-constexpr int kTensorsPerCu = 4;
+// MI355X, 2, 3, 4 and 8 workgroups per compute unit.  Partials: n = 3 x 10^7, k = 2
+// 23.7, 24.0, 25.6, 26.2 us; 1.5 x 10^7, k = 16 85.7, 83.2, 84.2, 88.6; 6 x 10^7, two
+// int8 30.2, 26.4, 27.4, 28.8; 8 x 10^8, k = 2 475, 478, 467, 473, k = 8 1990, 1911,
+// 1894, 1908 (1 per unit 2-25 % more than 2).  Lists: 200 MB 36.6, 38.7, 40.6, 39.9;
+// 600 MB 93.5, 97.6, 97.7, 101; 1.4 GB 215, 209, 214, 223; 4.2 GB 590, 608, 614, 623.
+// Fewer workgroups arrive sooner; too few do not keep enough loads in flight.
+constexpr int kPartialsPerCu = 3;
+constexpr int kTensorsPerCu = 2;
 
 // Bytes that a norm call reads last and with ordinary loads, for the step or the
 // scaling that follows to find in the last-level cache: its size.  The norm and

@@ -80,12 +80,13 @@ __device__ __forceinline__ bool last_of(uint32_t *counter, uint32_t size) {
 // caches, and a workgroup arrives only when its own has been acknowledged (the
 // wait).  Acquire and release on the arrivals would say the same at the price
 // of an L2 write-back and an invalidation per workgroup, which no other data
-// here needs: an empty kernel of 2048 workgroups with one counter took 52 us
-// that way and 27 us this way.  The rest is the arrivals' taking turns at one
-// address, about 12 ns each, so a large grid arrives at kCounters counters and
-// their last arrivals at one more: 5.6 us, where the empty kernel alone takes
-// 1.7 and a second launch would add about 3.5 (and 2.5 us on the host).  Up to
-// kOneCounter workgroups one counter is faster (64: 3.0 against 3.2 us).
+// here needs: an empty kernel of 1024 workgroups with one counter took 24.7 us
+// that way and 14.8 this way (2048: 52 and 27).  The rest is the arrivals' taking
+// turns at one address, about 12 ns each, so a large grid arrives at kCounters
+// counters and their last arrivals at one more: 4.3 us (2048: 5.6), where the
+// empty kernel alone takes 1.7 and a second launch would add about 3.5 (and 2.5 us
+// on the host).  Up to kOneCounter workgroups one counter is faster (64: 3.0
+// against 3.2 us).
 __device__ void finish(double s, const FinishArgs &f) {
     __shared__ int s_last;
     s = workgroup_sum(s);
