@@ -486,6 +486,7 @@ int norm_call(bool q8, const uint16_t *const *grads, const int8_t *const *qgrads
     const int64_t tile = norm_tile(k, q8);
     a.kept = kept_units(a.xcds, tile * k * (q8 ? 1 : 2));
     const int blocks = norm_blocks(dev, (n + tile - 1) / tile, kPartialsPerCu);
+    if (blocks < a.xcds) a.xcds = 1;  // every run needs a workgroup
     const hipError_t e = blocks > 0
                              ? launch_grad_norm(k, q8, a, blocks, (hipStream_t)stream)
                              : launch_finish(a.fin.sums, 0, r, clip, (hipStream_t)stream);
