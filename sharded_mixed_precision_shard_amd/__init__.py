@@ -887,8 +887,9 @@ class GradNorm:
     marshalled once, as ShardStep does for the step.  ``partials`` are bf16
     [n], or int8 [n] with their block scales ``qscales``; ``rule`` is a
     clip_rule or None, read at each call; ``clip`` the record it writes.  The
-    workspace is its own unless one is given, so keep the object until its
-    calls have run, and give calls on several streams an object each."""
+    workspace is its own unless a zeroed one (norm_workspace) is given, so keep
+    the object until its calls have run, and give calls on several streams an
+    object each."""
 
     def __init__(self, partials, n, rule, clip, grad_scale=1.0, qscales=None, workspace=None):
         lib = load_library()

@@ -770,21 +770,29 @@ int zs_tensor_pieces(const zs_tensor *tensors, int64_t count, zs_piece *pieces, 
     delete[] ranges;
     if (!clear) return ZS_ERR_ALIASING;
 
-    int64_t made = 0;
+    // a tensor has a piece for each stretch of kPieceBytes it touches
+    const auto end_of = [](const zs_tensor &x) {
+        return (uint64_t)(uintptr_t)x.data + (uint64_t)x.n * dtype_size((uint32_t)x.dtype);
+    };
+    int64_t total = 0;
+    for (int64_t i = 0; i < count; ++i)
+        if (tensors[i].n > 0)
+            total += (int64_t)((end_of(tensors[i]) - 1) / kPieceBytes -
+                               (uint64_t)(uintptr_t)tensors[i].data / kPieceBytes + 1);
+    *npieces = total;
+    if (!pieces) return ZS_OK;
+    if (total > capacity) return ZS_ERR_INVALID_ARGUMENT;
     for (int64_t i = 0; i < count; ++i) {
         const uint32_t dtype = (uint32_t)tensors[i].dtype;
         uint64_t a = (uint64_t)(uintptr_t)tensors[i].data;
-        const uint64_t end = a + (uint64_t)tensors[i].n * dtype_size(dtype);
+        const uint64_t end = end_of(tensors[i]);
         while (a < end) {
             const uint64_t cut = std::min(end, (a / kPieceBytes + 1) * (uint64_t)kPieceBytes);
-            if (pieces && made < capacity)
-                pieces[made] = {a, (uint32_t)((cut - a) / dtype_size(dtype)), dtype};
-            ++made;
+            *pieces++ = {a, (uint32_t)((cut - a) / dtype_size(dtype)), dtype};
             a = cut;
         }
     }
-    *npieces = made;
-    return pieces && made > capacity ? ZS_ERR_INVALID_ARGUMENT : ZS_OK;
+    return ZS_OK;
 }
 
 int zs_tensors_norm(const zs_tensor_table *table, const zs_clip_rule *rule, zs_clip *clip,

@@ -112,7 +112,14 @@ def test_pieces_refusals():
     assert lib.zs_tensor_pieces(one, 1, None, 0, None) == INVALID
     assert lib.zs_tensor_pieces(None, 1, None, 0, ctypes.byref(made)) == INVALID
     assert lib.zs_tensor_pieces(one, -1, None, 0, ctypes.byref(made)) == INVALID
-    one[0].reserved = 1
+    # a size no device holds is counted, not walked
+    one[0].n = 1 << 59
+    assert lib.zs_tensor_pieces(one, 1, None, 0, ctypes.byref(made)) == zs.ZS_OK
+    assert made.value == 1 << 48
+    assert lib.zs_tensor_pieces(one, 1, out, 39, ctypes.byref(made)) == INVALID
+    assert made.value == 1 << 48
+    assert lib.zs_tensor_pieces(one, 1, out, -1, ctypes.byref(made)) == INVALID
+    one[0].n, one[0].reserved = 10 * PIECE, 1
     assert lib.zs_tensor_pieces(one, 1, None, 0, ctypes.byref(made)) == INVALID
 
 
