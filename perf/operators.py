@@ -34,38 +34,38 @@ TYPES = {"bf16": (torch.bfloat16,), "fp16": (torch.float16,), "fp32": (torch.flo
 def listed():
     return [
         # a few thousand parameters on one rank: nothing but latency
-        dict(name="norm small shard", op="partials_norm", form="bf16", n=10007, k=3, ratio=0.5),
+        dict(name="norm, small shard", op="partials_norm", form="bf16", n=10007, k=3, ratio=0.5),
         # a 7B model on 8 ranks, one partial of each: heavy-tailed gradients
-        dict(name="norm 7B shard", op="partials_norm", form="bf16", n=805388288, k=8, ratio=0.5),
+        dict(name="norm, 7B shard", op="partials_norm", form="bf16", n=805388288, k=8, ratio=0.5),
         # a 175B model on 64 ranks, the partials of a quantized reduce-scatter
-        dict(name="norm 175B shard int8", op="partials_norm", form="int8", n=2718001152, k=2,
+        dict(name="norm, 175B shard int8", op="partials_norm", form="int8", n=2718001152, k=2,
              ratio=2.0),
         # replicated norm weights and biases, odd sizes
-        dict(name="norm small tensors", op="tensors_norm", types="fp32", count=41, total=200003,
+        dict(name="norm, small tensors", op="tensors_norm", types="fp32", count=41, total=200003,
              layout=1),
         # every gradient of a 0.7B model in bf16
-        dict(name="norm bf16 tensors", op="tensors_norm", types="bf16", count=292,
+        dict(name="norm, bf16 tensors", op="tensors_norm", types="bf16", count=292,
              total=708297600, layout=2),
         # gradients of three types, as where some layers accumulate in fp32
-        dict(name="norm mixed tensors", op="tensors_norm", types="mixed", count=301,
+        dict(name="norm, mixed tensors", op="tensors_norm", types="mixed", count=301,
              total=1600000007, layout=3),
         # the small tensors above, scaled
-        dict(name="clip small tensors", op="tensors_clip", types="fp32", count=41, total=200003,
+        dict(name="clip, small tensors", op="tensors_clip", types="fp32", count=41, total=200003,
              layout=1),
         # every gradient of a 0.7B model in bf16, scaled
-        dict(name="clip bf16 tensors", op="tensors_clip", types="bf16", count=292,
+        dict(name="clip, bf16 tensors", op="tensors_clip", types="bf16", count=292,
              total=708297600, layout=2),
         # a small model's step, four partials
-        dict(name="step small shard", op="clipped_step", form="base", n=1 << 20, k=4, segments=1,
+        dict(name="step, small shard", op="clipped_step", form="base", n=1 << 20, k=4, segments=1,
              ratio=0.5),
         # GPT-2-small on 8 ranks: the partials nearly fill the last-level cache
-        dict(name="step GPT-2-small shard", op="clipped_step", form="base", n=15554976, k=8,
+        dict(name="step, GPT-2-small shard", op="clipped_step", form="base", n=15554976, k=8,
              segments=27, ratio=0.5),
         # a 7B model on 8 ranks: the partials are read from memory both times
-        dict(name="step 7B shard", op="clipped_step", form="base", n=805388288, k=8, segments=32,
+        dict(name="step, 7B shard", op="clipped_step", form="base", n=805388288, k=8, segments=32,
              ratio=0.5),
         # a 175B model on 64 ranks with bf16 moments
-        dict(name="step 175B shard bf16 moments", op="clipped_step", form="bf16mv", n=2718001152,
+        dict(name="step, 175B shard bf16 moments", op="clipped_step", form="bf16mv", n=2718001152,
              k=2, segments=13, ratio=0.5),
     ]
 
