@@ -924,9 +924,18 @@ class GradNorm:
         return rc
 
 
+def _needs_workspace(workspace, name):
+    """Refuse a one-call norm without a workspace: one of its own would be free
+    again on return, while the kernel may still use it."""
+    if workspace is None:
+        raise ValueError("%s needs a workspace (norm_workspace); GradNorm and TensorsNorm keep one "
+                         "of their own" % name)
+
+
 def zs_grad_norm(grads, k, n, grad_scale, rule, clip, workspace, stream=None, check=True) -> int:
     """Enqueue the norm of the reduced gradient of k bf16 partials (see include/zs.h)."""
     _check_k(k, grads, "grads")
+    _needs_workspace(workspace, "zs_grad_norm")
     return GradNorm(grads, n, rule, clip, grad_scale, None, workspace)(stream, check)
 
 
@@ -934,6 +943,7 @@ def zs_grad_norm_q8grad(qgrads, qscales, k, n, grad_scale, rule, clip, workspace
                         check=True) -> int:
     """zs_grad_norm on int8 partials and their block scales."""
     _check_k(k, qgrads, "qgrads")
+    _needs_workspace(workspace, "zs_grad_norm_q8grad")
     return GradNorm(qgrads, n, rule, clip, grad_scale, qscales, workspace)(stream, check)
 
 
@@ -1036,6 +1046,7 @@ class TensorsNorm:
 
 def zs_tensors_norm(table, rule, clip, workspace, stream=None, check=True) -> int:
     """Enqueue the norm over a TensorTable's tensors (see include/zs.h)."""
+    _needs_workspace(workspace, "zs_tensors_norm")
     return TensorsNorm(table, rule, clip, workspace)(stream, check)
 
 
