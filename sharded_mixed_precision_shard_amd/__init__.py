@@ -750,6 +750,7 @@ class ShardStep:
         self._fn = fn
         self.variant = variant
         self._device = None
+        self._captured = _made_in_capture(clip)
         self._clipped = clip is not None
         if self._clipped:
             if cfg:
@@ -766,6 +767,8 @@ class ShardStep:
     def __call__(self, step, stream=None, check=True) -> int:
         if self._device is not None:
             _on_device(self._device)
+        if self._captured:
+            _graph_only("ShardStep(%s)" % self.variant)
         s = ctypes.c_void_p(_stream_handle(stream))
         if self._clipped:
             rc = self._fn(*self._head, int(step), *self._mid, *self._tail, s)
@@ -798,12 +801,31 @@ def clip_rule(max_norm, eps=1e-6, skip_nonfinite=False) -> ZsClipRule:
 
 def _zeroed(nbytes, device):
     """Zeroed device memory that any stream may use at once: the fill is waited
-    for (in a graph being captured it is a node of the graph instead)."""
+    for.  In a graph being captured it is a node of the graph instead, so the
+    memory holds anything until a replay; it is marked for _graph_only."""
     import torch
     buffer = torch.zeros(nbytes, dtype=torch.uint8, device=device)
-    if buffer.is_cuda and not torch.cuda.is_current_stream_capturing():
-        torch.cuda.current_stream(buffer.device).synchronize()
+    if buffer.is_cuda:
+        if torch.cuda.is_current_stream_capturing():
+            buffer.made_in_capture = True
+        else:
+            torch.cuda.current_stream(buffer.device).synchronize()
     return buffer
+
+
+def _made_in_capture(*xs) -> bool:
+    """Whether a record or workspace among xs was made during a capture."""
+    return any(getattr(x, "made_in_capture", False) for x in xs)
+
+
+def _graph_only(name):
+    """Refuse an eager call on a record or workspace made during a capture: its
+    zeroing is a node of that graph, so outside of it the arrival counters (or
+    coef and apply) may be anything."""
+    import torch
+    if not torch.cuda.is_current_stream_capturing():
+        raise ValueError("%s: a record or workspace made during a graph capture belongs to that "
+                         "graph; make it before the capture to use it in eager calls, too" % name)
 
 
 class ClipRecord:
@@ -811,11 +833,15 @@ class ClipRecord:
     zs_tensors_clip reads: one-element views ``sumsq`` (float64), ``norm``,
     ``coef`` (float32) and ``apply`` (int32) of it.  Reading one on the host
     waits for the GPU; an all-reduce of ``sumsq`` and zs_clip_combine do not.
-    Until the first norm call ``apply`` is 0, so nothing is clipped or stepped."""
+    Until the first norm call ``apply`` is 0, so nothing is clipped or stepped.
+    One made during a graph capture is set to zero by that graph's replays and
+    belongs to it: calls outside a capture refuse it.  Keep a record until the
+    calls on it have run."""
 
     def __init__(self, device="cuda"):
         import torch
         self.buffer = _zeroed(ctypes.sizeof(ZsClip), device)
+        self.made_in_capture = _made_in_capture(self.buffer)
         self.sumsq = self.buffer[0:8].view(torch.float64)
         self.norm = self.buffer[8:12].view(torch.float32)
         self.coef = self.buffer[12:16].view(torch.float32)
@@ -825,7 +851,8 @@ class ClipRecord:
 
 
 def norm_workspace(device="cuda"):
-    """Workspace of a norm call, zeroed; calls that may overlap in time need one each."""
+    """Workspace of a norm call, zeroed; calls that may overlap in time need one
+    each.  Made during a graph capture it belongs to that graph, as a ClipRecord does."""
     return _zeroed(ZS_NORM_WORKSPACE_BYTES, device)
 
 
@@ -902,6 +929,7 @@ class GradNorm:
         if workspace is None:
             workspace = norm_workspace("cuda" if self._device is None else self._device)
         self._keep = [list(partials), qscales, rule, clip, workspace]
+        self._captured = _made_in_capture(clip, workspace)
         if qscales is None:
             _check_type(partials, ("torch.bfloat16", "torch.int16", "torch.uint16"), "grads")
             self._c = (_ptr_array(partials, 2 * nn, "grads"),)
@@ -918,6 +946,8 @@ class GradNorm:
 
     def __call__(self, stream=None, check=True) -> int:
         _on_device(self._device)
+        if self._captured:
+            _graph_only(self._name)
         rc = self._fn(*self._args, _stream_handle(stream))
         if check and rc != ZS_OK:
             raise ZsError(rc, self._name)
@@ -956,6 +986,8 @@ def zs_clip_combine(sumsq, rule, clip, stream=None, count=None, check=True) -> i
         count = sumsq.numel() if count is None else count
     args = [_dev(sumsq, 8 * max(int(count), 0), "sumsq"), int(count), _rule(rule), _record(clip)]
     _on_device(_same_device([sumsq, clip]))
+    if getattr(clip, "made_in_capture", False):
+        _graph_only("zs_clip_combine")
     rc = load_library().zs_clip_combine(*args, _stream_handle(stream))
     if check and rc != ZS_OK:
         raise ZsError(rc, "zs_clip_combine")
@@ -1008,7 +1040,8 @@ class TensorTable:
     """A list of GPU tensors (bf16, fp16 and fp32 mixed; dense, any alignment)
     for zs_tensors_norm and zs_tensors_clip.  Its pieces are copied to the
     device here, on the current stream; the tensors are referenced for the
-    object's lifetime and must keep their memory (no resize, no new ``.data``)."""
+    object's lifetime and must keep their memory (no resize, no new ``.data``).
+    Keep the table until the calls on it have run."""
 
     def __init__(self, tensors):
         import torch
@@ -1032,12 +1065,15 @@ class TensorsNorm:
         if workspace is None:
             workspace = norm_workspace("cuda" if self._device is None else self._device)
         self._keep = [table, rule, clip, workspace]
+        self._captured = _made_in_capture(clip, workspace)
         self._fn = load_library().zs_tensors_norm
         self._args = [ctypes.byref(table.table), _rule(rule), _record(clip),
                       _dev(workspace, ZS_NORM_WORKSPACE_BYTES, "workspace")]
 
     def __call__(self, stream=None, check=True) -> int:
         _on_device(self._device)
+        if self._captured:
+            _graph_only("zs_tensors_norm")
         rc = self._fn(*self._args, _stream_handle(stream))
         if check and rc != ZS_OK:
             raise ZsError(rc, "zs_tensors_norm")
@@ -1053,6 +1089,8 @@ def zs_tensors_norm(table, rule, clip, workspace, stream=None, check=True) -> in
 def zs_tensors_clip(table, clip, stream=None, check=True) -> int:
     """Enqueue the scaling of a TensorTable's tensors by the record's coef, in place."""
     _on_device(_same_device([clip, table]))
+    if getattr(clip, "made_in_capture", False):
+        _graph_only("zs_tensors_clip")
     rc = load_library().zs_tensors_clip(ctypes.byref(table.table), _record(clip),
                                         _stream_handle(stream))
     if check and rc != ZS_OK:
