@@ -1,0 +1,63 @@
+"""The clipping recipes of README.md, run as they are printed on a stream that is
+not torch's current one, as one of three ranks (the all-reduce, a stand-in, finds
+the same sum on each), against the unclipped step with the coefficient in its
+grad_scale.
+
+Tolerance.  The total and its norm as in the norm's own tests; the product with
+the three ranks is one rounding of binary64 more, far below 2^-34."""
+import math
+import os
+import re
+
+import numpy as np
+import pytest
+
+import sharded_mixed_precision_shard_amd as zs
+from tests.conftest import ROOT
+from tests.test_gpu_clipped_step import Shard, hp_of, same
+from tests.test_gpu_norm import REL, fold, gpu, reference, rule_of  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+N, K, T, RANKS, SCALE = 70_001, 3, 12, 3, 0.25
+
+
+def recipes():
+    text = open(os.path.join(ROOT, "README.md")).read()
+    return [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "zs." in b]
+
+
+@pytest.fixture
+def job(gpu, monkeypatch):
+    """What a program has in hand before the recipes, as their names."""
+    torch, stream = gpu, gpu.cuda.Stream()
+    s = Shard(torch, "base", N, K, 9)
+    s.tensors = [torch.randn(777, device="cuda"), torch.randn(64, 9, device="cuda").half()]
+    stream.wait_stream(torch.cuda.current_stream())
+
+    def all_reduce(x):
+        # a collective orders itself with the current stream
+        assert torch.cuda.current_stream() == stream
+        x.mul_(RANKS)
+
+    monkeypatch.setattr(torch.distributed, "all_reduce", all_reduce)
+    names = dict(zs=zs, torch=torch, device="cuda", stream=stream, partials=s.grads, n=N, k=K, t=T,
+                 master=s.master, m=s.dm, v=s.dv, param=s.param, segments=s.table,
+                 hparams=hp_of(SCALE), grad_scale=SCALE, tensors=s.tensors, lr=1e-3, beta1=0.9,
+                 beta2=0.95, eps=1e-8, decay=0.1, host_master=s.w.copy(), host_m=s.m.copy(),
+                 host_v=s.v.copy(), host_param=np.zeros(N, np.uint16), host_partials=s.bits,
+                 host_segments=s.segs)
+    return torch, s, names
+
+
+def test_one_total_over_the_ranks(job):
+    torch, s, names = job
+    exec(recipes()[0], names)
+    torch.cuda.synchronize()
+    total = RANKS * reference(fold(s.values, SCALE))[0]
+    _, coef = rule_of(total, 1.0, float(np.float32(1e-6)))
+    got = names["record"].coef.item()
+    assert coef < 1 and abs(got - coef) <= REL * coef
+    other = Shard(torch, "base", N, K, 9)
+    other.step(hp_of(float(np.float32(SCALE) * np.float32(got))))(T)
+    assert same(torch, s.outputs(), other.outputs())
