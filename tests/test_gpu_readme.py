@@ -61,3 +61,22 @@ def test_one_total_over_the_ranks(job):
     other = Shard(torch, "base", N, K, 9)
     other.step(hp_of(float(np.float32(SCALE) * np.float32(got))))(T)
     assert same(torch, s.outputs(), other.outputs())
+
+
+def test_tensors_outside_the_shard_count_once(job):
+    torch, s, names = job
+    before = [x.clone() for x in s.tensors]
+    exec(recipes()[0].split("with torch")[0], names)
+    exec(recipes()[1], names)
+    torch.cuda.synchronize()
+    total = RANKS * reference(fold(s.values, SCALE))[0] + \
+        sum(reference(x.double().cpu().numpy())[0] for x in before)
+    norm, coef = rule_of(total, 1.0, float(np.float32(1e-6)))
+    record = names["record"]
+    assert abs(record.norm.item() - norm) <= REL * norm
+    assert coef < 1 and abs(record.coef.item() - coef) <= REL * coef
+    for x, b in zip(s.tensors, before):
+        assert torch.equal(x, (b.float() * record.coef).to(b.dtype))
+    other = Shard(torch, "base", N, K, 9)
+    other.step(hp_of(float(np.float32(SCALE) * np.float32(record.coef.item()))))(T)
+    assert same(torch, s.outputs(), other.outputs())
