@@ -80,3 +80,27 @@ def test_tensors_outside_the_shard_count_once(job):
     other = Shard(torch, "base", N, K, 9)
     other.step(hp_of(float(np.float32(SCALE) * np.float32(record.coef.item()))))(T)
     assert same(torch, s.outputs(), other.outputs())
+
+
+def test_host_step_and_its_skip(job):
+    torch, s, names = job
+    hosts = [names["host_" + x] for x in ("master", "m", "v", "param")]
+    start = [h.copy() for h in hosts]
+    exec(recipes()[0], names)
+    exec(recipes()[2], names)
+    for dev, host in zip((s.master, s.dm, s.dv, s.param), hosts):
+        assert np.array_equal(dev.cpu().numpy().view(np.uint8), host.view(np.uint8))
+    # an infinity: nothing steps, on the device or the host
+    for h, a in zip(hosts, start):
+        h[...] = a
+    device = [x.clone() for x in s.outputs()]
+    s.grads[1][N - 1] = 0x7f80
+    s.bits[1][N - 1] = 0x7f80
+    torch.cuda.synchronize()
+    exec(recipes()[0], names)
+    exec(recipes()[2], names)
+    torch.cuda.synchronize()
+    assert names["record"].norm.item() == math.inf and names["record"].apply.item() == 0
+    assert same(torch, s.outputs(), device)
+    for h, a in zip(hosts, start):
+        assert np.array_equal(h.view(np.uint8), a.view(np.uint8))
