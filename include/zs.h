@@ -393,22 +393,27 @@ int zs_unpack_state_bf16mv(const float *state, float *master, uint16_t *m_bf16, 
  * and rounded once to binary32.  The order of the sum is fixed by the sizes
  * and the device, so the same call gives the same bits.
  *
- * Infinities and NaN: S is then infinite or NaN.  An infinite norm gives coef
- * 0 (which turns infinite elements into NaN and the others into 0), a NaN norm
- * coef NaN.  With rule->skip_nonfinite set, apply is 0 instead whenever the
- * norm is not finite, and the clipped step and zs_tensors_clip then leave every
- * buffer as it was: the step is skipped, as loss scaling wants it.
+ * Infinities and NaN among the elements make S infinite or NaN.  A NaN norm
+ * gives coef NaN.  An infinite norm gives coef 0 (which turns infinite elements
+ * into NaN and the others into 0) under a finite max_norm, and coef 1 under an
+ * infinite one.  S may also be finite and its root above what binary32 holds:
+ * norm is then infinite, while coef, formed in binary64, is as defined and may
+ * be above 0.  With rule->skip_nonfinite set, apply is 0 whenever `norm` as it
+ * stands in the record is not finite (the last case included), and the clipped
+ * step and zs_tensors_clip then leave every buffer as it was: the step is
+ * skipped, as loss scaling wants it.
  */
 typedef struct {
     double sumsq;   /* S */
-    float norm;     /* sqrt(S) */
+    float norm;     /* sqrt(S), infinite where binary32 cannot hold it */
     float coef;     /* what a clipped gradient is multiplied by, 0 .. 1 */
     int32_t apply;  /* 0: a clipped step or zs_tensors_clip changes nothing; 1: it runs */
     int32_t reserved;
 } zs_clip;          /* DEVICE record, 8-byte aligned */
 
-/* max_norm >= 0, may be infinite (coef is then 1); eps >= 0 and finite.  A
- * null rule stands for an infinite max_norm and skip_nonfinite 0. */
+/* max_norm >= 0, may be infinite (coef is then 1, or NaN where the norm is);
+ * eps >= 0 and finite.  A null rule stands for an infinite max_norm, eps 0 and
+ * skip_nonfinite 0. */
 typedef struct {
     float max_norm;
     float eps;
@@ -539,8 +544,9 @@ int zs_tensors_norm(const zs_tensor_table *table, const zs_clip_rule *rule, zs_c
 
 /* Scale every element of the table's tensors in place by clip->coef: x becomes
  * f32(x) * coef in binary32, rounded to the tensor's type (to nearest even; NaN
- * -> 0x7FC0 in bf16).  With apply 0 or coef exactly 1 nothing is read or written
- * (x * 1 = x).  HBM traffic: the tensors read and written once. */
+ * -> 0x7FC0 in bf16).  The record lies apart from the tensors.  With apply 0 or
+ * coef exactly 1 nothing is read or written (x * 1 = x).  HBM traffic: the
+ * tensors read and written once. */
 int zs_tensors_clip(const zs_tensor_table *table, const zs_clip *clip, void *stream);
 
 /* Release what zs_init recorded.  Later calls return ZS_ERR_NOT_INITIALIZED

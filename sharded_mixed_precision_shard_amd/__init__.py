@@ -795,7 +795,8 @@ def zs_shard_step_clipped(variant, master, m, v, param_bf16, grads, n, seg_table
 def clip_rule(max_norm, eps=1e-6, skip_nonfinite=False) -> ZsClipRule:
     """The clipping rule: coef = 1 where norm + eps <= max_norm, else
     max_norm / (norm + eps); ``skip_nonfinite`` makes the clipped step and
-    zs_tensors_clip leave everything as it was when the norm is not finite."""
+    zs_tensors_clip leave everything as it was when the record's norm is not finite
+    (a norm above binary32's range among them)."""
     return ZsClipRule(max_norm, eps, 1 if skip_nonfinite else 0, 0)
 
 
