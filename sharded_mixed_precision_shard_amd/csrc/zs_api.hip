@@ -422,6 +422,14 @@ int norm_blocks(int dev, int64_t units, int per_cu) {
 constexpr int kPartialsPerCu = 3;
 constexpr int kTensorsPerCu = 2;
 
+// In the XCD-contiguous order every run has a workgroup: what pair_runs takes has
+// at least kMaxXcds tiles (a tile is at most 64 KB of partials, or 2^15 elements),
+// and norm_blocks gives them a workgroup each, or half of the cap and more.
+constexpr int kMaxXcds = 8;
+static_assert(kPairRunsMinBytes / (kThreads * 16 * ZS_MAX_K) >= kMaxXcds);
+static_assert(kXcdOrderMinElems / norm_tile(1, true) >= kMaxXcds);
+static_assert(kPartialsPerCu / 2 >= 1);
+
 // Bytes that a norm call reads last and with ordinary loads, for the step or the
 // scaling that follows to find in the last-level cache: its size.  The norm and
 // the step after it, three sets of buffers in turn, with 0, 64, 128, 192 and 256 MB:
@@ -486,7 +494,6 @@ int norm_call(bool q8, const uint16_t *const *grads, const int8_t *const *qgrads
     const int64_t tile = norm_tile(k, q8);
     a.kept = kept_units(a.xcds, tile * k * (q8 ? 1 : 2));
     const int blocks = norm_blocks(dev, (n + tile - 1) / tile, kPartialsPerCu);
-    if (blocks < a.xcds) a.xcds = 1;  // every run needs a workgroup
     const hipError_t e = blocks > 0
                              ? launch_grad_norm(k, q8, a, blocks, (hipStream_t)stream)
                              : launch_finish(a.fin.sums, 0, r, clip, (hipStream_t)stream);
