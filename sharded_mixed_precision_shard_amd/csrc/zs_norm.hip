@@ -212,10 +212,13 @@ __device__ __forceinline__ void each_backwards(const Share &s, int64_t kept, F f
     for (; t >= s.begin; t -= s.stride) f(t, std::true_type());
 }
 
-// Scaled: grad_scale is not 1 (g * 1 = g, so the product may be left out).  With
-// few partials, int8 above all, the kernel is as near the VALU's limit as
-// HBM's, and the product is one of five operations per element: 2.7 x 10^9
-// int8 elements, one partial 478 us with it and 417 without, two 885 and 820.
+// Scaled: with the product by grad_scale; g * 1 = g, so it may be left out where
+// that is 1.  The int8 kernels have a form without it: with few partials they are
+// as near the VALU's limit as HBM's, and the product is one of five operations per
+// element.  2.4 GB, without and with it: one partial 393 and 443 us, two 371 and
+// 381, three to seven 0.4-1.5 % apart, eight and more 0.1-0.6 %.  The bf16 kernels
+// always multiply: at every k from 1 to 16 both took the same time (2.4 GB: 342-353
+// us, 0.4 % apart at most and either way; 200 MB: 32-34 us).
 template <int K, bool Q8, bool Scaled>
 __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const NormArgs a) {
     typedef PartialVectors<K, Q8> Vec;
@@ -423,11 +426,9 @@ __global__ __launch_bounds__(kThreads) void finish_kernel(const double *sums, in
 
 template <int K>
 static const void *norm_kernel(bool q8, bool scaled) {
-    if (q8)
-        return scaled ? (const void *)grad_norm_kernel<K, true, true>
-                      : (const void *)grad_norm_kernel<K, true, false>;
-    return scaled ? (const void *)grad_norm_kernel<K, false, true>
-                  : (const void *)grad_norm_kernel<K, false, false>;
+    if (!q8) return (const void *)grad_norm_kernel<K, false, true>;
+    return scaled ? (const void *)grad_norm_kernel<K, true, true>
+                  : (const void *)grad_norm_kernel<K, true, false>;
 }
 
 hipError_t launch_grad_norm(int k, bool q8, const NormArgs &a, int blocks, hipStream_t stream) {
