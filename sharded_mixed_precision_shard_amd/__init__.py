@@ -53,10 +53,10 @@ EXPORTS = ("zs_init", "zs_shard_step", "zs_shard_step_cfg", "zs_shard_step_q8ag"
            "zs_shard_step_packed_q8ag", "zs_shard_step_packed_q8grad",
            "zs_shard_step_packed_bf16mv", "zs_shard_step_bf16mv_sr",
            "zs_shard_step_packed_bf16mv_sr", "zs_pack_state", "zs_unpack_state",
-           "zs_pack_state_bf16mv", "zs_unpack_state_bf16mv", "zs_grad_norm",
-           "zs_grad_norm_q8grad", "zs_clip_combine", "zs_shard_step_clipped", "zs_tensor_pieces", "zs_tensors_norm",
-           "zs_tensors_clip", "zs_fini", "zs_status_string", "zs_last_device_error", "zs_algorithmic_bytes", "zs_launch_geometry",
-           "zs_launch_plan")
+           "zs_pack_state_bf16mv", "zs_unpack_state_bf16mv", "zs_grad_norm", "zs_grad_norm_q8grad",
+           "zs_clip_combine", "zs_shard_step_clipped", "zs_tensor_pieces", "zs_tensors_norm",
+           "zs_tensors_clip", "zs_fini", "zs_status_string", "zs_last_device_error",
+           "zs_algorithmic_bytes", "zs_launch_geometry", "zs_launch_plan")
 
 
 def packed_floats(n: int) -> int:

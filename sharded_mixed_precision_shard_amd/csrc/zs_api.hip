@@ -142,13 +142,18 @@ int resolve_launch(int k, int64_t n, int variant, const zs_launch_cfg *cfg,
 // per element (4 bf16, 8 int8) and 4 MB in all.  Both calls then read an element
 // on the same XCD, and what the norm read last is still in its L2 (32 MB over
 // the device) when the step starts there.  Norm and step, linear and
-// XCD-contiguous, three sets of buffers in turn: k = 4, n = 7 x 10^5 11.9 and
-// 10.9 us, 2^20 14.9 and 13.0, 2 x 10^7 134 and 129, 6 x 10^7 412 and 414; k = 8,
+// XCD-contiguous, three sets of buffers in turn, by calls: k = 4, n = 7 x 10^5 11.9
+// and 10.9 us, 2^20 14.9 and 13.0, 2 x 10^7 134 and 129, 6 x 10^7 412 and 414; k = 8,
 // 1.3 x 10^6 20.2 and 18.4, 7.7 x 10^6 77.4 and 73.9; k = 16, 1.3 x 10^6 27.2 and 23.9;
-// the other forms alike.  With one or two bf16 partials it goes either way at
-// 10^6 elements (12.2 and 11.5 us, 11.9 and 11.7) and loses 2-5 % from 3 x 10^6 on,
-// with four int8 ones 2-4 % from 7 x 10^6 on; with 3 x 10^5 elements it gains
-// nothing up to k = 8.
+// the other forms alike.  On another machine, a graph of the pair: k = 4, 1.5 x 10^6
+// 23.4 and 22.4, 7 x 10^6 57.9 and 56.2, 2 x 10^7 135 and 131, 6 x 10^7 399 and 404;
+// eight int8, 2 x 10^7 152 and 146, 6 x 10^7 435 and 424.  The border is not sharp:
+// below it k = 3 would gain up to 2 x 10^7 (1.5 x 10^6 22.3 and 20.8, 2 x 10^7 123.0
+// and 122.4) and lose at 6 x 10^7 (356 and 365; bf16 moments 285 and 283), six int8
+// gain 0-6 % at every size (2 x 10^7 130 and 128), seven 1-7 % from 10^6 on (146 and
+// 135), and five lose 2 to gain 5 %.  With one or two bf16 partials it goes either way
+// at 10^6 elements (12.2 and 11.5 us, 11.9 and 11.7) and loses 2-5 % from 3 x 10^6 on,
+// with four int8 ones 1-4 %; with 3 x 10^5 elements it gains nothing up to k = 8.
 constexpr int kPairRunsMinPerElem = 8;
 constexpr int64_t kPairRunsMinBytes = int64_t(1) << 22;
 
@@ -418,14 +423,16 @@ int norm_blocks(int dev, int64_t units, int per_cu) {
 // int8 30.2, 26.4, 27.4, 28.8; 8 x 10^8, k = 2 475, 478, 467, 473, k = 8 1990, 1911,
 // 1894, 1908 (1 per unit 2-25 % more than 2).  Lists: 200 MB 36.6, 38.7, 40.6, 39.9;
 // 600 MB 93.5, 97.6, 97.7, 101; 1.4 GB 215, 209, 214, 223; 4.2 GB 590, 608, 614, 623.
-// Fewer workgroups arrive sooner; too few do not keep enough loads in flight.
+// Fewer workgroups arrive sooner; too few do not keep enough loads in flight.  One
+// number serves every size: 3 for partials and 2 for lists are within 3 % of the best
+// at each of these; partials of 8 x 10^8 elements take 1-2 % less with 4.
 constexpr int kPartialsPerCu = 3;
 constexpr int kTensorsPerCu = 2;
 
 // In the XCD-contiguous order every run has a workgroup: what pair_runs takes has
 // at least kMaxXcds tiles (a tile is at most 64 KB of partials, or 2^15 elements),
 // and norm_blocks gives them a workgroup each, or half of the cap and more.
-constexpr int kMaxXcds = 8;
+constexpr int kMaxXcds = 8;  // MI355X
 static_assert(kPairRunsMinBytes / (kThreads * 16 * ZS_MAX_K) >= kMaxXcds);
 static_assert(kXcdOrderMinElems / norm_tile(1, true) >= kMaxXcds);
 static_assert(kPartialsPerCu / 2 >= 1);
