@@ -139,10 +139,14 @@ int resolve_launch(int k, int64_t n, int variant, const zs_launch_cfg *cfg,
 
 // The order of a norm call and of the clipped step after it: XCD-contiguous for
 // shards that the step takes so anyway, and below them for partials of 8 bytes
-// per element (4 bf16, 8 int8) and 4 MB in all.  Both calls then read an element
-// on the same XCD, and what the norm read last is still in its L2 (32 MB over
-// the device) when the step starts there.  Norm and step, linear and
-// XCD-contiguous, three sets of buffers in turn, by calls: k = 4, n = 7 x 10^5 11.9
+// per element (4 bf16, 8 int8) and 4 MB in all.  Both calls then read an element on
+// the same XCD, where its L2 (32 MB over the device) can still hold what the norm
+// read last.  What the pair takes less than its two kernels alone, linear and
+// XCD-contiguous: 7.7 x 10^6 elements, k = 8 6.4 and 13.1 us, 2 x 10^7, k = 4 11.3 and
+// 21.1 (the last-level cache gives the first of each, and the step alone is 2-5 us
+// slower in this order there); at 2^20, k = 4 the order itself helps, the step alone
+// takes 9.5 and 7.9 us.  Norm and step, linear and XCD-contiguous, three sets of
+// buffers in turn, by calls: k = 4, n = 7 x 10^5 11.9
 // and 10.9 us, 2^20 14.9 and 13.0, 2 x 10^7 134 and 129, 6 x 10^7 412 and 414; k = 8,
 // 1.3 x 10^6 20.2 and 18.4, 7.7 x 10^6 77.4 and 73.9; k = 16, 1.3 x 10^6 27.2 and 23.9;
 // the other forms alike.  On another machine, a graph of the pair: k = 4, 1.5 x 10^6
