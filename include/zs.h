@@ -35,7 +35,8 @@
  *
  * Beside the step: the norm of the gradient over all parameters, clipping by
  * it, and the step on the clipped gradient ("Global gradient norm and
- * clipping" below).
+ * clipping" below); and 4- and 8-bit copies of parameters and activations with
+ * the products of a linear layer on them ("Microscaled formats" below).
  *
  * Threading: zs_init/zs_fini must not race with other calls.  After
  * zs_init the library holds no mutable state, so zs_shard_step may be
@@ -548,6 +549,107 @@ int zs_tensors_norm(const zs_tensor_table *table, const zs_clip_rule *rule, zs_c
  * coef exactly 1 nothing is read or written (x * 1 = x).  HBM traffic: the
  * tensors read and written once. */
 int zs_tensors_clip(const zs_tensor_table *table, const zs_clip *clip, void *stream);
+
+/*
+ * Microscaled formats, and the linear layer on them.
+ *
+ * A matrix is held in blocks of ZS_MX_BLOCK elements along each row: one byte
+ * b per block for the power of two 2^(b - 127) (b = 255 stands for NaN), and
+ * per element a floating-point code of 4 bits (ZS_MX_FP4, E2M1: 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 and their negatives) or of 8 (ZS_MX_FP8, E4M3: up to 448).  An
+ * element is its code's value times its block's power of two: 4.25 or 8.25
+ * bits per element.  Uses beside the step:
+ *  - the parameter copy for a 4-bit all-gather, made of param_bf16 and read by
+ *    the receivers' products as it is.  A shard is a matrix of one long row; a
+ *    weight of the flat buffer that begins at a multiple of ZS_MX_BLOCK and
+ *    whose rows are whole blocks has its own blocks in it, at codes + start / 2
+ *    (fp4) and scales + start / 32;
+ *  - an activation kept in 8 bits from the forward to the backward pass, where
+ *    the weight's gradient is made from it: a bf16 partial for the norm and the
+ *    step, or fp32 sums over several batches.
+ *
+ * codes holds ZS_MX_ROW_BYTES(format, cols) bytes per row, whole blocks: element
+ * i of a row is in its byte i (fp8) or in byte i / 2 (fp4; the low four bits for
+ * even i).  The codes past the row's end are zero, and zs_mx_quantize writes
+ * them so; zs_mx_product reads them.  scales holds ceil(cols / ZS_MX_BLOCK)
+ * bytes per row.
+ */
+#define ZS_MX_BLOCK 32
+#define ZS_MX_FP4 0
+#define ZS_MX_FP8 1
+#define ZS_MX_ROW_BYTES(format, cols) \
+    (((int64_t)(cols) + 31) / 32 * ((format) == ZS_MX_FP4 ? 16 : 32))
+
+typedef struct {
+    uint8_t *codes;   /* DEVICE, 16-byte aligned */
+    uint8_t *scales;  /* DEVICE */
+    int64_t rows, cols;
+    int32_t format;   /* ZS_MX_* */
+    int32_t reserved; /* must be 0 */
+} zs_mx;
+
+/* A dense matrix: rows ld elements apart, ld >= cols. */
+typedef struct {
+    void *data;       /* DEVICE, aligned to the element's size */
+    int64_t rows, cols, ld;
+    int32_t dtype;    /* ZS_DTYPE_* */
+    int32_t reserved; /* must be 0 */
+} zs_matrix;
+
+/*
+ * Quantise x (bf16, fp16 or fp32) into the blocks of `out`, of the same rows and
+ * cols.  With a the largest magnitude of a block,
+ *   E = floor(log2 a) - 2 (fp4) or - 8 (fp8), at least -127;  b = E + 127
+ * and an element's code is the nearest to x * 2^-E, ties to the even code,
+ * values past the format's largest saturated to it.  A block of zeros has b = 0;
+ * one with an infinity or a NaN has b = 255 and codes 0, so it reads back as NaN.
+ * zs_mx_dequantize writes each element's value, rounded once to out's type (to
+ * nearest even; exact in fp32, and in bf16 down to its smallest denormal).
+ *
+ * The spans of matrix, codes and scales must not overlap (ZS_ERR_ALIASING).
+ * zero rows or cols: ZS_OK, nothing enqueued.  At most 2^32 - 1 blocks.  One
+ * kernel and nothing else is enqueued, and errors are reported synchronously
+ * before that; the arguments are checked before the state of the library.
+ */
+int zs_mx_quantize(const zs_matrix *x, const zs_mx *out, void *stream);
+int zs_mx_dequantize(const zs_mx *x, const zs_matrix *out, void *stream);
+
+/*
+ * The linear layer y = x w^T with w [N, K] in blocks (either format), and its
+ * backward pass:
+ *   zs_mx_linear        y [M, N]  = x [M, K] w^T     x bf16
+ *   zs_mx_product       y [M, N]  = x [M, K] w^T     x in blocks (either format)
+ *   zs_mx_linear_dgrad  dx [M, K] = dy [M, N] w      dy bf16
+ *   zs_mx_linear_wgrad  dw [N, K] = dy [M, N]^T x    dy bf16, x [M, K] in blocks;
+ *                       with add = 1 (fp32 only) dw += ...
+ * y, dx and dw are bf16 or fp32 and written whole (rows ld elements apart: the
+ * gaps are left as they were).  A sum over no elements is 0.
+ *
+ * Numerics: a block's elements are exact in bf16 (see zs_mx_dequantize), so are
+ * the products in fp32, and the sums are fp32; each output is rounded once to its
+ * type.  The order of a sum is fixed by the sizes, the device and whether there
+ * is a workspace: the same call gives the same bits.  Infinities and NaN go
+ * where the formula takes them; an element that the layout pads takes no part.
+ *
+ *   workspace : DEVICE memory of the caller, ZS_MX_WORKSPACE_BYTES, 16-byte
+ *               aligned, set to zero once before its first call (each call
+ *               leaves it ready for the next), or NULL.  With it a product of
+ *               few output tiles splits its sum over more of the device.  Calls
+ *               that may run at the same time (other streams, graphs replayed
+ *               side by side) need one each.
+ * The span of the output must not overlap an input, nor the workspace anything
+ * (ZS_ERR_ALIASING).  M, N and K up to 2^28, outputs up to 2^36 elements.
+ * Capture and errors as for zs_mx_quantize.
+ */
+#define ZS_MX_WORKSPACE_BYTES 67108864
+int zs_mx_linear(const zs_matrix *x, const zs_mx *w, const zs_matrix *y, void *workspace,
+                 void *stream);
+int zs_mx_product(const zs_mx *x, const zs_mx *w, const zs_matrix *y, void *workspace,
+                  void *stream);
+int zs_mx_linear_dgrad(const zs_matrix *dy, const zs_mx *w, const zs_matrix *dx, void *workspace,
+                       void *stream);
+int zs_mx_linear_wgrad(const zs_matrix *dy, const zs_mx *x, const zs_matrix *dw, int add,
+                       void *workspace, void *stream);
 
 /* Release what zs_init recorded.  Later calls return ZS_ERR_NOT_INITIALIZED
  * until zs_init is called again.  Always returns ZS_OK. */

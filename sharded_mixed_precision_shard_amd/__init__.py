@@ -13,7 +13,9 @@ Entry points keep the C names: :func:`zs_init`, :func:`zs_shard_step`,
 :func:`zs_shard_step_packed_bf16mv_sr`, :func:`zs_pack_state`, :func:`zs_unpack_state`,
 :func:`zs_pack_state_bf16mv`, :func:`zs_unpack_state_bf16mv`, :func:`zs_grad_norm`,
 :func:`zs_grad_norm_q8grad`, :func:`zs_clip_combine`, :func:`zs_shard_step_clipped`,
-:func:`zs_tensor_pieces`, :func:`zs_tensors_norm`, :func:`zs_tensors_clip`, :func:`zs_fini`,
+:func:`zs_tensor_pieces`, :func:`zs_tensors_norm`, :func:`zs_tensors_clip`,
+:func:`zs_mx_quantize`, :func:`zs_mx_dequantize`, :func:`zs_mx_linear`, :func:`zs_mx_product`,
+:func:`zs_mx_linear_dgrad`, :func:`zs_mx_linear_wgrad`, :func:`zs_fini`,
 :func:`zs_status_string`, :func:`zs_last_device_error`, :func:`zs_algorithmic_bytes`,
 :func:`zs_launch_geometry`, :func:`zs_launch_plan`.
 """
@@ -33,8 +35,12 @@ ZS_Q8_BLOCK = 256
 ZS_MAX_GROUPS_PER_CU = 32
 ZS_NORM_WORKSPACE_BYTES = 65536
 ZS_MAX_SUMS = 65536
+ZS_MX_BLOCK = 32
+ZS_MX_WORKSPACE_BYTES = 67108864
 
 ZS_DTYPE = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
+
+ZS_MX_FORMAT = {"fp4": 0, "fp8": 1}
 
 ZS_OK = 0
 ZS_ERR_NOT_INITIALIZED = 1
@@ -55,8 +61,10 @@ EXPORTS = ("zs_init", "zs_shard_step", "zs_shard_step_cfg", "zs_shard_step_q8ag"
            "zs_shard_step_packed_bf16mv_sr", "zs_pack_state", "zs_unpack_state",
            "zs_pack_state_bf16mv", "zs_unpack_state_bf16mv", "zs_grad_norm", "zs_grad_norm_q8grad",
            "zs_clip_combine", "zs_shard_step_clipped", "zs_tensor_pieces", "zs_tensors_norm",
-           "zs_tensors_clip", "zs_fini", "zs_status_string", "zs_last_device_error",
-           "zs_algorithmic_bytes", "zs_launch_geometry", "zs_launch_plan")
+           "zs_tensors_clip", "zs_mx_quantize", "zs_mx_dequantize", "zs_mx_linear",
+           "zs_mx_product", "zs_mx_linear_dgrad", "zs_mx_linear_wgrad", "zs_fini",
+           "zs_status_string", "zs_last_device_error", "zs_algorithmic_bytes",
+           "zs_launch_geometry", "zs_launch_plan")
 
 
 def packed_floats(n: int) -> int:
@@ -125,6 +133,17 @@ class ZsPiece(ctypes.Structure):
 
 class ZsTensorTable(ctypes.Structure):
     _fields_ = [("pieces", ctypes.c_void_p), ("count", ctypes.c_int64)]
+
+
+class ZsMx(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("format", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class ZsMatrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class ZsError(RuntimeError):
@@ -202,6 +221,14 @@ def load_library():
     lib.zs_tensors_norm.restype = ctypes.c_int
     lib.zs_tensors_clip.argtypes = [P, P, P]
     lib.zs_tensors_clip.restype = ctypes.c_int
+    lib.zs_mx_quantize.argtypes = [P, P, P]
+    lib.zs_mx_dequantize.argtypes = [P, P, P]
+    for name in ("zs_mx_linear", "zs_mx_product", "zs_mx_linear_dgrad"):
+        getattr(lib, name).argtypes = [P, P, P, P, P]
+    lib.zs_mx_linear_wgrad.argtypes = [P, P, P, ctypes.c_int, P, P]
+    for name in ("zs_mx_quantize", "zs_mx_dequantize", "zs_mx_linear", "zs_mx_product",
+                 "zs_mx_linear_dgrad", "zs_mx_linear_wgrad"):
+        getattr(lib, name).restype = ctypes.c_int
     lib.zs_fini.argtypes = []
     lib.zs_fini.restype = ctypes.c_int
     lib.zs_status_string.argtypes = [ctypes.c_int]
@@ -1176,3 +1203,168 @@ def zs_host_max_threads() -> int:
 
 def zs_host_isa() -> str:
     return load_host_library().zs_host_isa().decode()
+
+
+# ---------------------------------- microscaled formats and the linear layer
+
+def mx_row_bytes(format: str, cols: int) -> int:
+    """Bytes of a row's codes (ZS_MX_ROW_BYTES)."""
+    return -(-int(cols) // ZS_MX_BLOCK) * (16 if format == "fp4" else 32)
+
+
+class Mx:
+    """A matrix held in blocks of 32 elements along its rows (see include/zs.h):
+    ``codes`` and ``scales`` are uint8 tensors of mx_row_bytes(format, cols) and
+    ceil(cols / 32) bytes a row, ``format`` is "fp4" (E2M1) or "fp8" (E4M3).  The
+    tensors are referenced for the object's lifetime.  :meth:`empty` makes them."""
+
+    def __init__(self, codes, scales, cols, format):
+        if format not in ZS_MX_FORMAT:
+            raise ValueError("format: expected 'fp4' or 'fp8', got %r" % (format,))
+        _check_type((codes,), ("torch.uint8",), "codes")
+        _check_type((scales,), ("torch.uint8",), "scales")
+        cols = int(cols)
+        if cols < 0:
+            raise ValueError("cols must not be negative")
+        blocks, width = -(-cols // ZS_MX_BLOCK), mx_row_bytes(format, cols)
+        rows = scales.numel() // blocks if blocks else int(scales.shape[0])
+        if scales.numel() != rows * blocks or codes.numel() != rows * width:
+            raise ValueError("codes hold %d bytes and scales %d: no whole rows of %d and %d"
+                             % (codes.numel(), scales.numel(), width, blocks))
+        self.codes, self.scales, self.format = codes, scales, format
+        self.rows, self.cols, self.shape = rows, cols, (rows, cols)
+        self.device = codes.device
+        self.index = _same_device((codes, scales))
+        self.struct = ZsMx(_dev(codes, rows * width, "codes"),
+                           _dev(scales, rows * blocks, "scales"), rows, cols,
+                           ZS_MX_FORMAT[format], 0)
+
+    @classmethod
+    def empty(cls, rows, cols, format, device="cuda"):
+        """Room for a matrix of the given size, to be written by zs_mx_quantize."""
+        import torch
+        if format not in ZS_MX_FORMAT:
+            raise ValueError("format: expected 'fp4' or 'fp8', got %r" % (format,))
+        codes = torch.empty((rows, mx_row_bytes(format, cols)), dtype=torch.uint8, device=device)
+        scales = torch.empty((rows, -(-int(cols) // ZS_MX_BLOCK)), dtype=torch.uint8,
+                             device=device)
+        return cls(codes, scales, cols, format)
+
+    def part(self, start, rows, cols):
+        """The matrix of [rows, cols] at element ``start`` of this one, which is one
+        long row (a shard): a weight's blocks in the gathered parameters.  start and
+        cols are multiples of 32."""
+        start, rows, cols = int(start), int(rows), int(cols)
+        if self.rows != 1 or start % ZS_MX_BLOCK or cols % ZS_MX_BLOCK:
+            raise ValueError("a part is cut from one row, at multiples of %d" % ZS_MX_BLOCK)
+        if start < 0 or rows < 0 or cols < 0 or start + rows * cols > self.cols:
+            raise ValueError("[%d, %d] elements from %d on are not inside %d"
+                             % (rows, cols, start, self.cols))
+        each = mx_row_bytes(self.format, ZS_MX_BLOCK)
+        a, b = start // ZS_MX_BLOCK, (start + rows * cols) // ZS_MX_BLOCK
+        codes = self.codes.reshape(-1)[a * each:b * each]
+        scales = self.scales.reshape(-1)[a:b]
+        return Mx(codes.view(rows, mx_row_bytes(self.format, cols)),
+                  scales.view(rows, cols // ZS_MX_BLOCK), cols, self.format)
+
+
+_MATRIX_TYPE = {**ZS_DTYPE, "torch.int16": 0, "torch.uint16": 0}
+
+
+def _matrix(x, name) -> ZsMatrix:
+    """A GPU tensor as a zs_matrix: two dimensions (or one: a single row), the
+    elements of a row side by side, rows any distance apart.  16-bit integers are
+    bf16 patterns, as the step writes them."""
+    if not getattr(x, "is_cuda", False):
+        raise ValueError("%s must be a GPU tensor (got %s)" % (name, getattr(x, "device",
+                                                                             type(x))))
+    dtype = _MATRIX_TYPE.get(_type_name(x.dtype))
+    if dtype is None:
+        raise TypeError("%s: %s is not bfloat16, float16 or float32" % (name, x.dtype))
+    if x.dim() == 1:
+        rows, cols, step, ld = 1, x.shape[0], x.stride(0), x.shape[0]
+    elif x.dim() == 2:
+        (rows, cols), (ld, step) = x.shape, x.stride()
+        if rows <= 1:
+            ld = cols
+    else:
+        raise ValueError("%s must have one or two dimensions, not %d" % (name, x.dim()))
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise ValueError("%s: a row's elements must lie side by side and rows apart (strides %s)"
+                         % (name, tuple(x.stride())))
+    return ZsMatrix(x.data_ptr(), rows, cols, max(ld, cols), dtype, 0)
+
+
+def mx_workspace(device="cuda"):
+    """Workspace of the products, zeroed; calls that may overlap in time need one
+    each.  Made during a graph capture it belongs to that graph, as a ClipRecord does."""
+    return _zeroed(ZS_MX_WORKSPACE_BYTES, device)
+
+
+def _held(x, name) -> ZsMx:
+    if not isinstance(x, Mx):
+        raise TypeError("%s: expected an Mx, got %r" % (name, type(x)))
+    return x.struct
+
+
+def _mx_call(name, tensors, workspace, args, stream, check) -> int:
+    """Enqueue a call of the microscaled formats on tensors of one device."""
+    index = _same_device([*tensors, workspace])
+    _on_device(index)
+    if _made_in_capture(workspace):
+        _graph_only(name)
+    rc = getattr(load_library(), name)(*args, _stream_handle(stream))
+    if check and rc != ZS_OK:
+        raise ZsError(rc, name)
+    return rc
+
+
+def zs_mx_quantize(x, out, stream=None, check=True) -> int:
+    """Quantise the matrix x (bf16, fp16 or fp32) into the blocks of ``out``, an Mx
+    of its size."""
+    return _mx_call("zs_mx_quantize", (x, out), None,
+                    (ctypes.byref(_matrix(x, "x")), ctypes.byref(_held(out, "out"))), stream,
+                    check)
+
+
+def zs_mx_dequantize(x, out, stream=None, check=True) -> int:
+    """Write the values of an Mx into a matrix of its size (bf16, fp16 or fp32)."""
+    return _mx_call("zs_mx_dequantize", (x, out), None,
+                    (ctypes.byref(_held(x, "x")), ctypes.byref(_matrix(out, "out"))), stream,
+                    check)
+
+
+def _mx_space(workspace):
+    return None if workspace is None else _dev(workspace, ZS_MX_WORKSPACE_BYTES, "workspace")
+
+
+def zs_mx_linear(x, w, y, stream=None, workspace=None, check=True) -> int:
+    """y [M, N] = x [M, K] w^T for a bf16 x and an Mx w [N, K]; y is bf16 or fp32.
+    With a ``workspace`` (mx_workspace) a product of few output tiles splits its
+    sum over more of the device."""
+    return _mx_call("zs_mx_linear", (x, w, y), workspace,
+                    (ctypes.byref(_matrix(x, "x")), ctypes.byref(_held(w, "w")),
+                     ctypes.byref(_matrix(y, "y")), _mx_space(workspace)), stream, check)
+
+
+def zs_mx_product(x, w, y, stream=None, workspace=None, check=True) -> int:
+    """zs_mx_linear of an x that is an Mx itself."""
+    return _mx_call("zs_mx_product", (x, w, y), workspace,
+                    (ctypes.byref(_held(x, "x")), ctypes.byref(_held(w, "w")),
+                     ctypes.byref(_matrix(y, "y")), _mx_space(workspace)), stream, check)
+
+
+def zs_mx_linear_dgrad(dy, w, dx, stream=None, workspace=None, check=True) -> int:
+    """dx [M, K] = dy [M, N] w for a bf16 dy and an Mx w [N, K]; dx is bf16 or fp32."""
+    return _mx_call("zs_mx_linear_dgrad", (dy, w, dx), workspace,
+                    (ctypes.byref(_matrix(dy, "dy")), ctypes.byref(_held(w, "w")),
+                     ctypes.byref(_matrix(dx, "dx")), _mx_space(workspace)), stream, check)
+
+
+def zs_mx_linear_wgrad(dy, x, dw, add=False, stream=None, workspace=None, check=True) -> int:
+    """dw [N, K] = dy [M, N]^T x for a bf16 dy and the activation x [M, K] kept as an
+    Mx; dw is bf16 (a partial of the step) or fp32, where ``add`` adds to it."""
+    return _mx_call("zs_mx_linear_wgrad", (dy, x, dw), workspace,
+                    (ctypes.byref(_matrix(dy, "dy")), ctypes.byref(_held(x, "x")),
+                     ctypes.byref(_matrix(dw, "dw")), int(bool(add)), _mx_space(workspace)),
+                    stream, check)

@@ -1,6 +1,7 @@
 """Build the gfx950 shared library ``libzs.so`` from ``csrc/zs_kernels.hip``
-(the step kernels), ``csrc/zs_norm.hip`` (the norm and scaling kernels) and
-``csrc/zs_api.hip`` (the C ABI), and ``libzs_host.so``.
+(the step kernels), ``csrc/zs_norm.hip`` (the norm and scaling kernels),
+``csrc/zs_mx.hip`` (the microscaled formats' kernels), ``csrc/zs_api.hip`` and
+``csrc/zs_mx_api.hip`` (the C ABI), and ``libzs_host.so``.
 
 hipcc cross-compiles for gfx950 without a GPU, so this runs anywhere the
 ROCm toolchain is installed.  The library is built in-tree, next to this file.
@@ -16,6 +17,8 @@ REPO_DIR = os.path.dirname(PKG_DIR)
 INCLUDE_DIR = os.path.join(REPO_DIR, "include")
 SRCS = [os.path.join(PKG_DIR, "csrc", "zs_kernels.hip"),
         os.path.join(PKG_DIR, "csrc", "zs_norm.hip"),
+        os.path.join(PKG_DIR, "csrc", "zs_mx.hip"),
+        os.path.join(PKG_DIR, "csrc", "zs_mx_api.hip"),
         os.path.join(PKG_DIR, "csrc", "zs_api.hip")]
 # The sources the kernels are compiled from (their hash keys measured traffic).
 KERNEL_SRCS = [os.path.join(PKG_DIR, "csrc", "zs_kernels.hip"),

@@ -15,6 +15,7 @@
 
 #include "zs.h"
 #include "zs_kernels.h"
+#include "zs_mx.h"
 #include "zs_norm.h"
 
 namespace {
@@ -536,6 +537,15 @@ Request base_request(float *master, void *m, void *v, uint16_t *param, int k, in
 }
 
 }  // namespace
+
+int zs_detail::mx_device(MxDevice *out) {
+    int dev = 0;
+    const int st = current_device(&dev);
+    if (st == ZS_OK) *out = {g_dev[dev].cus, g_dev[dev].xcds};
+    return st;
+}
+
+int zs_detail::mx_launched(hipError_t e) { return e == hipSuccess ? ZS_OK : device_error(e); }
 
 extern "C" {
 

@@ -1,0 +1,640 @@
+// zs_mx.hip -- kernels of the microscaled formats: quantisation, dequantisation
+// and the products of a linear layer on them.
+//
+// A block is 32 elements along a row with one power of two 2^(b - 127).  Its
+// elements are E2M1 (fp4) or E4M3 (fp8) numbers, both exact in bf16, and so is
+// their product by the power of two (down to bf16's smallest denormal): the
+// products below feed bf16 matrix instructions without any rounding of the
+// stored operand, and sum in fp32.
+
+#include <type_traits>
+
+#include "zs_mx.h"
+
+namespace zs_detail {
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Vectors at any address that suits their elements.
+struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
+struct __attribute__((packed, aligned(2))) Any8 { uint64_t v; };
+
+__device__ __forceinline__ float scale_of(uint32_t b) { return __uint_as_float(b << 23); }
+
+__device__ __forceinline__ uint32_t bits(bf16x2 v) { return __builtin_bit_cast(uint32_t, v); }
+
+// 8 codes as bf16 times the scale: fp4 in one word, fp8 in two.
+__device__ __forceinline__ u32x4 widen_fp4(uint32_t w, float s) {
+    return u32x4{bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0)),
+                 bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1)),
+                 bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2)),
+                 bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3))};
+}
+__device__ __forceinline__ u32x4 widen_fp8(uint32_t w0, uint32_t w1, float s) {
+    return u32x4{bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false)),
+                 bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true)),
+                 bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false)),
+                 bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true))};
+}
+
+// ------------------------------------------------ quantisation, dequantisation
+
+// Four lanes take a block, 8 elements each; a workgroup takes kCastUnroll times
+// 64 blocks.  Bound by memory: bf16 to fp8 moves 3.03 bytes per element, to fp4
+// 2.53, against about 3 vector instructions per element.
+constexpr int kCastUnroll = 4;
+constexpr int kCastBlocks = kCastUnroll * kThreads / 4;
+
+template <int DT>
+__device__ __forceinline__ void load8(const void *x, int64_t at, int64_t left, float v[8]) {
+    if constexpr (DT == ZS_DTYPE_FP32) {
+        const float *p = (const float *)x + at;
+        if (left >= 8) {
+            const u32x4 a = ((const Any16 *)p)->v, b = ((const Any16 *)(p + 4))->v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = __uint_as_float(a[e]);
+                v[e + 4] = __uint_as_float(b[e]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < left ? p[e] : 0.0f;
+        }
+    } else {
+        const uint16_t *p = (const uint16_t *)x + at;
+        u32x4 a = {0, 0, 0, 0};
+        if (left >= 8) {
+            a = ((const Any16 *)p)->v;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < left) a[e / 2] |= (uint32_t)p[e] << (16 * (e % 2));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t h = (a[e / 2] >> (16 * (e % 2))) & 0xffffu;
+            if constexpr (DT == ZS_DTYPE_BF16)
+                v[e] = __uint_as_float(h << 16);
+            else
+                v[e] = (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+        }
+    }
+}
+
+// Largest of the four lanes that share a block.
+__device__ __forceinline__ uint32_t block_max(uint32_t m) {
+    const uint32_t a = (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xf, 0xf, true);
+    m = m > a ? m : a;
+    const uint32_t b = (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xf, 0xf, true);
+    return m > b ? m : b;
+}
+
+template <int FMT, int DT>
+__global__ __launch_bounds__(kThreads) void mx_quantize(MxCastArgs a) {
+    const int part = threadIdx.x % 4;
+    const int64_t first = (int64_t)blockIdx.x * kCastBlocks + threadIdx.x / 4;
+    float v[kCastUnroll][8];
+#pragma unroll
+    for (int u = 0; u < kCastUnroll; ++u) {
+        const int64_t block = first + u * (kThreads / 4);
+        const int64_t row = a.nb < a.blocks ? block / a.nb : 0;
+        const int64_t col = (block - row * a.nb) * kMxBlock + part * 8;
+        load8<DT>(a.x, row * a.ld + col, block < a.blocks ? a.cols - col : 0, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kCastUnroll; ++u) {
+        const int64_t block = first + u * (kThreads / 4);
+        // magnitudes order as their bits do, infinity and NaN above every number
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = __float_as_uint(v[u][e]) & 0x7fffffffu;
+            m = m > b ? m : b;
+        }
+        m = block_max(m);
+        const bool finite = m < 0x7f800000u;
+        constexpr int top = FMT == ZS_MX_FP4 ? 2 : 8;
+        const int e = (int)(m >> 23) - top;
+        const uint32_t b = e > 0 ? (uint32_t)e : 0u;  // the biased exponent of the scale
+        const float inv = finite ? __uint_as_float((254u - b) << 23) : 0.0f;
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            q[i] = finite ? v[u][i] * inv : 0.0f;
+            // E4M3 has no infinity to saturate at: 448 is its largest value
+            if constexpr (FMT == ZS_MX_FP8) q[i] = __builtin_amdgcn_fmed3f(q[i], -448.0f, 448.0f);
+        }
+        if (block < a.blocks) {
+            if constexpr (FMT == ZS_MX_FP4) {
+                uint32_t w = 0;
+                w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[0], q[1], 1.0f, 0);
+                w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[2], q[3], 1.0f, 1);
+                w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[4], q[5], 1.0f, 2);
+                w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[6], q[7], 1.0f, 3);
+                ((uint32_t *)a.codes)[block * 4 + part] = w;
+            } else {
+                s16x2 lo = {0, 0}, hi = {0, 0};
+                lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, q[0], q[1], 1.0f, false);
+                lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, q[2], q[3], 1.0f, true);
+                hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, q[4], q[5], 1.0f, false);
+                hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, q[6], q[7], 1.0f, true);
+                ((uint2 *)a.codes)[block * 4 + part] =
+                    uint2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+            }
+            if (part == 0) a.scales[block] = finite ? (uint8_t)b : 255;
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void *x, int64_t at, int64_t left, const float v[8]) {
+    if constexpr (DT == ZS_DTYPE_FP32) {
+        float *p = (float *)x + at;
+        if (left >= 8) {
+            ((Any16 *)p)->v = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                    __float_as_uint(v[2]), __float_as_uint(v[3])};
+            ((Any16 *)(p + 4))->v = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                          __float_as_uint(v[6]), __float_as_uint(v[7])};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < left) p[e] = v[e];
+        }
+    } else {
+        uint16_t *p = (uint16_t *)x + at;
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if constexpr (DT == ZS_DTYPE_BF16)
+                h[e] = __builtin_bit_cast(uint16_t, (__bf16)v[e]);
+            else
+                h[e] = __builtin_bit_cast(uint16_t, (_Float16)v[e]);
+        }
+        if (left >= 8) {
+            ((Any16 *)p)->v = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                                    h[6] | h[7] << 16};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < left) p[e] = (uint16_t)h[e];
+        }
+    }
+}
+
+template <int FMT, int DT>
+__global__ __launch_bounds__(kThreads) void mx_dequantize(MxCastArgs a) {
+    const int part = threadIdx.x % 4;
+    const int64_t first = (int64_t)blockIdx.x * kCastBlocks + threadIdx.x / 4;
+    uint2 code[kCastUnroll];
+    uint32_t scale[kCastUnroll];
+#pragma unroll
+    for (int u = 0; u < kCastUnroll; ++u) {
+        const int64_t block = first + u * (kThreads / 4);
+        code[u] = uint2{0, 0};
+        scale[u] = 0;
+        if (block < a.blocks) {
+            if constexpr (FMT == ZS_MX_FP4)
+                code[u].x = ((const uint32_t *)a.codes)[block * 4 + part];
+            else
+                code[u] = ((const uint2 *)a.codes)[block * 4 + part];
+            scale[u] = a.scales[block];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kCastUnroll; ++u) {
+        const int64_t block = first + u * (kThreads / 4);
+        const int64_t row = a.nb < a.blocks ? block / a.nb : 0;
+        const int64_t col = (block - row * a.nb) * kMxBlock + part * 8;
+        const float s = scale_of(scale[u]);
+        f32x2 w[4];
+        if constexpr (FMT == ZS_MX_FP4) {
+            w[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[u].x, s, 0);
+            w[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[u].x, s, 1);
+            w[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[u].x, s, 2);
+            w[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code[u].x, s, 3);
+        } else {
+            w[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(code[u].x, s, false);
+            w[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(code[u].x, s, true);
+            w[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(code[u].y, s, false);
+            w[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(code[u].y, s, true);
+        }
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = w[e / 2][e % 2];
+        if (block < a.blocks) store8<DT>(a.x, row * a.ld + col, a.cols - col, v);
+    }
+}
+
+// ------------------------------------------------------------------ products
+
+constexpr int kStep = 64;  // c's per step: two blocks of a stored row
+
+// A tile in LDS holds bf16, kStep c's of B rows.  Row-major (c along a row):
+// 128 bytes a row, its eight 16-byte chunks in an order that the row's number
+// permutes, so that the 32 rows of a fragment read spread over the banks.
+// Column-major (c a row of B elements): the 64-byte chunks of a row permuted by
+// c for the same reason.
+__device__ __forceinline__ int at_rows(int row, int chunk) {
+    return row * 128 + ((chunk ^ (row & 7)) << 4);
+}
+template <int B>
+__device__ __forceinline__ int at_cols(int c, int byte) {
+    if constexpr (B >= 256)
+        return c * (B * 2) + (byte ^ ((c & 7) << 6));
+    else if constexpr (B == 128)
+        return c * (B * 2) + (byte ^ ((c & 3) << 6));
+    else
+        return c * (B * 2) + (byte ^ (((c >> 1) & 1) << 6));
+}
+
+// The 8 c's of a 32x32x16 fragment that a lane holds: c = 16 s + 8 (lane / 32) ..
+// of row base + lane % 32.
+__device__ __forceinline__ bf16x8 frag_rows(const char *lds, int base, int s, int lane) {
+    const int row = base + lane % 32;
+    return *(const bf16x8 *)(lds + at_rows(row, 2 * s + lane / 32));
+}
+// The same from a column-major tile: of 16 lanes each reads 8 bytes of row
+// (lane % 16) / 4, and the transposing read hands lane i the elements i of four rows.
+template <int B>
+__device__ __forceinline__ bf16x8 frag_cols(const char *lds, int base, int s, int lane) {
+    typedef s16x4 __attribute__((address_space(3))) * lds_s16x4;
+    const int t = lane % 16;
+    const int c = 16 * s + 8 * (lane / 32) + t / 4;
+    const int byte = (base + (lane / 16) % 2 * 16 + (t % 4) * 4) * 2;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_s16x4)(lds + at_cols<B>(c, byte)));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_s16x4)(lds + at_cols<B>(c + 4, byte)));
+    const short v __attribute__((ext_vector_type(8))) = {lo[0], lo[1], lo[2], lo[3],
+                                                         hi[0], hi[1], hi[2], hi[3]};
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+// What a thread carries of a bf16 operand from memory to LDS.  COLS: c is the row.
+template <int B, int NT, bool COLS>
+struct PlainStage {
+    static constexpr int kChunks = B * kStep / 8;
+    static constexpr int kEach = kChunks / NT;
+    u32x4 r[kEach];
+
+    __device__ __forceinline__ void load(const uint16_t *p, int64_t ld, int first, int rows, int c0,
+                                         int C, int tid) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int q = k * NT + tid;
+            int64_t row, col;
+            int left;
+            if constexpr (COLS) {
+                const int c = c0 + q / (B / 8), i = first + q % (B / 8) * 8;
+                row = c;
+                col = i;
+                left = c < C ? rows - i : 0;
+            } else {
+                const int i = first + q / 8, c = c0 + q % 8 * 8;
+                row = i;
+                col = c;
+                left = i < rows ? C - c : 0;
+            }
+            const uint16_t *x = p + row * ld + col;
+            u32x4 v = {0, 0, 0, 0};
+            if (left >= 8) {
+                v = ((const Any16 *)x)->v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < left) v[e / 2] |= (uint32_t)x[e] << (16 * (e % 2));
+            }
+            r[k] = v;
+        }
+    }
+    __device__ __forceinline__ void store(char *lds, int tid) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int q = k * NT + tid;
+            const int at = COLS ? at_cols<B>(q / (B / 8), q % (B / 8) * 16) : at_rows(q / 8, q % 8);
+            *(u32x4 *)(lds + at) = r[k];
+        }
+    }
+};
+
+// The same of an operand in blocks: a unit is one block, widened to bf16 on its way.
+template <int B, int NT, bool COLS, bool F8>
+struct HeldStage {
+    static constexpr int kUnits = B * kStep / kMxBlock;
+    static constexpr int kEach = (kUnits + NT - 1) / NT;
+    u32x4 r[kEach][F8 ? 2 : 1];
+    uint32_t scale[kEach];
+
+    __device__ __forceinline__ void load(const MxHeld &x, int first, int rows, int c0, int C,
+                                         int tid) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int q = k * NT + tid;
+            int64_t row, block;
+            bool in;
+            if constexpr (COLS) {
+                row = c0 + q / (B / kMxBlock);
+                block = first / kMxBlock + q % (B / kMxBlock);
+                in = row < C;
+            } else {
+                row = first + q / 2;
+                block = c0 / kMxBlock + q % 2;
+                in = row < rows;
+            }
+            r[k][0] = u32x4{0, 0, 0, 0};
+            if constexpr (F8) r[k][1] = u32x4{0, 0, 0, 0};
+            scale[k] = 127;
+            if (in && block < x.nb && q < kUnits) {
+                const int64_t at = row * x.nb + block;
+                const u32x4 *codes = (const u32x4 *)x.codes + at * (F8 ? 2 : 1);
+                r[k][0] = codes[0];
+                if constexpr (F8) r[k][1] = codes[1];
+                scale[k] = x.scales[at];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(char *lds, int tid) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int q = k * NT + tid;
+            if (kUnits % NT != 0 && q >= kUnits) continue;
+            const float s = scale_of(scale[k]);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                u32x4 v;
+                if constexpr (F8)
+                    v = widen_fp8(r[k][w / 2][w % 2 * 2], r[k][w / 2][w % 2 * 2 + 1], s);
+                else
+                    v = widen_fp4(r[k][0][w], s);
+                const int at = COLS ? at_cols<B>(q / (B / kMxBlock),
+                                                 q % (B / kMxBlock) * 64 + w * 16)
+                                    : at_rows(q / 2, q % 2 * 4 + w);
+                *(u32x4 *)(lds + at) = v;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+    return bits(v);
+}
+
+// Four values of out[i, j ..], added to what is there where the call says so.
+__device__ __forceinline__ void put4(const MxProductArgs &a, int i, int j, f32x4 v) {
+    if (i >= a.I || j >= a.J) return;
+    const int64_t at = (int64_t)i * a.ldo + j;
+    if (a.out_f32) {
+        float *o = (float *)a.out + at;
+        if (j + 4 <= a.J) {
+            if (a.add) v += __builtin_bit_cast(f32x4, ((const Any16 *)o)->v);
+            ((Any16 *)o)->v = __builtin_bit_cast(u32x4, v);
+        } else {
+            for (int e = 0; e < 4 && j + e < a.J; ++e) o[e] = a.add ? o[e] + v[e] : v[e];
+        }
+    } else {
+        uint16_t *o = (uint16_t *)a.out + at;
+        const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+        if (j + 4 <= a.J) {
+            ((Any8 *)o)->v = (uint64_t)hi << 32 | lo;
+        } else {
+            for (int e = 0; e < 4 && j + e < a.J; ++e)
+                o[e] = (uint16_t)((e < 2 ? lo : hi) >> (16 * (e % 2)));
+        }
+    }
+}
+
+// Which of a tile's splits arrives last: it finds the others' sums in memory.
+// All threads call it after they have written theirs.
+__device__ __forceinline__ bool last_split(uint32_t *counter, int splits, uint32_t *shared) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t before =
+            __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        const bool last = before == (uint32_t)splits - 1u;
+        if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *shared = last;
+    }
+    __syncthreads();
+    const bool last = *shared != 0;
+    if (last) __threadfence();
+    return last;
+}
+
+// A workgroup makes a BI x BJ tile of out (of one split of c).  The matrix
+// instruction takes Q's rows as its rows and P's as its columns: a lane then
+// holds four neighbouring j's of one i, and stores them together.
+template <int BI, int BJ, int WI, int WJ, int LEFT, int RIGHT>
+__global__ __launch_bounds__(WI *WJ *kWave) void mx_tile(MxProductArgs a) {
+    constexpr int NT = WI * WJ * kWave;
+    constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
+    constexpr bool PC = LEFT == kLeftCols, QC = (RIGHT & kRightCols) != 0;
+    constexpr bool P_HELD = LEFT == kLeftFp4 || LEFT == kLeftFp8;
+    constexpr int P_BYTES = BI * kStep * 2, Q_BYTES = BJ * kStep * 2;
+    __shared__ __attribute__((aligned(128))) char lds[2 * (P_BYTES + Q_BYTES)];
+
+    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+    const int i0 = tile % a.tiles_i * BI, j0 = tile / a.tiles_i * BJ;
+    const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+    const int first = split * a.split_steps;
+    const int steps = min((a.C + kStep - 1) / kStep - first, a.split_steps);
+
+    f32x16 acc[FJ][FI];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int i = 0; i < FI; ++i) acc[j][i] = f32x16{};
+
+    std::conditional_t<P_HELD, HeldStage<BI, NT, false, LEFT == kLeftFp8>,
+                       PlainStage<BI, NT, PC>> ps;
+    HeldStage<BJ, NT, QC, (RIGHT & kRightFp8) != 0> qs;
+    auto load = [&](int step) {
+        const int c0 = (first + step) * kStep;
+        if constexpr (P_HELD)
+            ps.load(a.px, i0, a.I, c0, a.C, tid);
+        else
+            ps.load(a.p, a.ldp, i0, a.I, c0, a.C, tid);
+        qs.load(a.q, j0, a.J, c0, a.C, tid);
+    };
+    auto store = [&](int buffer) {
+        char *p = lds + buffer * (P_BYTES + Q_BYTES);
+        ps.store(p, tid);
+        qs.store(p + P_BYTES, tid);
+    };
+    if (steps > 0) {
+        load(0);
+        store(0);
+    }
+    for (int step = 0; step < steps; ++step) {
+        const bool more = step + 1 < steps;
+        if (more) load(step + 1);
+        __syncthreads();
+        const char *p = lds + step % 2 * (P_BYTES + Q_BYTES), *q = p + P_BYTES;
+#pragma unroll
+        for (int s = 0; s < kStep / 16; ++s) {
+            bf16x8 pf[FI], qf[FJ];
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+                pf[i] = PC ? frag_cols<BI>(p, wi + 32 * i, s, lane)
+                           : frag_rows(p, wi + 32 * i, s, lane);
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+                qf[j] = QC ? frag_cols<BJ>(q, wj + 32 * j, s, lane)
+                           : frag_rows(q, wj + 32 * j, s, lane);
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int i = 0; i < FI; ++i)
+                    acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[j], pf[i], acc[j][i], 0,
+                                                                        0, 0);
+        }
+        if (more) store((step + 1) % 2);
+    }
+
+    // lane: i = lane % 32, and for each r four j's from 8 r + 4 (lane / 32)
+    const int li = wi + lane % 32, lj = wj + lane / 32 * 4;
+    if (a.splits > 1) {
+        float *mine = a.parts + ((int64_t)tile * a.splits + split) * (BI * BJ);
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *(f32x4 *)(mine + (((wave * FJ + j) * FI + i) * 4 + r) * 256 + lane * 4) =
+                        f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
+                              acc[j][i][4 * r + 3]};
+        if (!last_split(a.counters + tile, a.splits, (uint32_t *)lds)) return;
+        const float *parts = a.parts + (int64_t)tile * a.splits * (BI * BJ);
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float *at =
+                        parts + (((wave * FJ + j) * FI + i) * 4 + r) * 256 + lane * 4;
+                    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int k = 0; k < a.splits; ++k)  // always in this order
+                        v += *(const f32x4 *)(at + (int64_t)k * (BI * BJ));
+                    put4(a, i0 + li + 32 * i, j0 + lj + 32 * j + 8 * r, v);
+                }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                put4(a, i0 + li + 32 * i, j0 + lj + 32 * j + 8 * r,
+                     f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
+                           acc[j][i][4 * r + 3]});
+}
+
+template <int BI, int BJ, int WI, int WJ, int LEFT, int RIGHT>
+hipError_t run_tile(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
+    a.tiles_i = (a.I + BI - 1) / BI;
+    a.tiles_j = (a.J + BJ - 1) / BJ;
+    const int64_t tiles = (int64_t)a.tiles_i * a.tiles_j;
+    const int steps = (a.C + kStep - 1) / kStep;
+    int64_t splits = 1;
+    if (workspace && tiles <= kMxCounters && tiles < dev.cus) {
+        splits = dev.cus / tiles;
+        splits = splits < steps / 8 ? splits : steps / 8;
+        const int64_t room = kMxPartBytes / (tiles * BI * BJ * 4);
+        splits = splits < room ? splits : room;
+        splits = splits > 1 ? splits : 1;
+    }
+    a.split_steps = steps > 0 ? (int)((steps + splits - 1) / splits) : 0;
+    a.splits = steps > 0 ? (steps + a.split_steps - 1) / a.split_steps : 1;
+    a.counters = (uint32_t *)workspace;
+    a.parts = (float *)((char *)workspace + kMxCounterBytes);
+    mx_tile<BI, BJ, WI, WJ, LEFT, RIGHT>
+        <<<dim3((uint32_t)(tiles * a.splits)), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <int LEFT, int RIGHT>
+hipError_t choose_tile(const MxProductArgs &a, void *workspace, const MxDevice &dev,
+                       hipStream_t stream) {
+    if ((int64_t)a.I * a.J >= (int64_t)dev.cus * 128 * 128)
+        return run_tile<128, 128, 2, 2, LEFT, RIGHT>(a, workspace, dev, stream);
+    return run_tile<64, 64, 2, 2, LEFT, RIGHT>(a, workspace, dev, stream);
+}
+
+
+template <int FMT, int DT>
+hipError_t run_quantize(const MxCastArgs &a, hipStream_t stream) {
+    const int64_t groups = (a.blocks + kCastBlocks - 1) / kCastBlocks;
+    mx_quantize<FMT, DT><<<dim3((uint32_t)groups), dim3(kThreads), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <int FMT, int DT>
+hipError_t run_dequantize(const MxCastArgs &a, hipStream_t stream) {
+    const int64_t groups = (a.blocks + kCastBlocks - 1) / kCastBlocks;
+    mx_dequantize<FMT, DT><<<dim3((uint32_t)groups), dim3(kThreads), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(int format, int dtype, const MxCastArgs &a, hipStream_t stream) {
+    switch (format * 3 + dtype) {
+        case 0: return run_quantize<ZS_MX_FP4, ZS_DTYPE_BF16>(a, stream);
+        case 1: return run_quantize<ZS_MX_FP4, ZS_DTYPE_FP16>(a, stream);
+        case 2: return run_quantize<ZS_MX_FP4, ZS_DTYPE_FP32>(a, stream);
+        case 3: return run_quantize<ZS_MX_FP8, ZS_DTYPE_BF16>(a, stream);
+        case 4: return run_quantize<ZS_MX_FP8, ZS_DTYPE_FP16>(a, stream);
+        default: return run_quantize<ZS_MX_FP8, ZS_DTYPE_FP32>(a, stream);
+    }
+}
+
+hipError_t launch_mx_dequantize(int format, int dtype, const MxCastArgs &a, hipStream_t stream) {
+    switch (format * 3 + dtype) {
+        case 0: return run_dequantize<ZS_MX_FP4, ZS_DTYPE_BF16>(a, stream);
+        case 1: return run_dequantize<ZS_MX_FP4, ZS_DTYPE_FP16>(a, stream);
+        case 2: return run_dequantize<ZS_MX_FP4, ZS_DTYPE_FP32>(a, stream);
+        case 3: return run_dequantize<ZS_MX_FP8, ZS_DTYPE_BF16>(a, stream);
+        case 4: return run_dequantize<ZS_MX_FP8, ZS_DTYPE_FP16>(a, stream);
+        default: return run_dequantize<ZS_MX_FP8, ZS_DTYPE_FP32>(a, stream);
+    }
+}
+
+hipError_t launch_mx_product(MxLeft left, int right, MxProductArgs a, void *workspace,
+                             const MxDevice &dev, hipStream_t stream) {
+    constexpr int c4 = kRightFp4 | kRightCols, c8 = kRightFp8 | kRightCols;
+    switch (left * 4 + right) {
+        case kLeftRows * 4 + kRightFp4:
+            return choose_tile<kLeftRows, kRightFp4>(a, workspace, dev, stream);
+        case kLeftRows * 4 + kRightFp8:
+            return choose_tile<kLeftRows, kRightFp8>(a, workspace, dev, stream);
+        case kLeftRows * 4 + c4: return choose_tile<kLeftRows, c4>(a, workspace, dev, stream);
+        case kLeftRows * 4 + c8: return choose_tile<kLeftRows, c8>(a, workspace, dev, stream);
+        case kLeftCols * 4 + c4: return choose_tile<kLeftCols, c4>(a, workspace, dev, stream);
+        case kLeftCols * 4 + c8: return choose_tile<kLeftCols, c8>(a, workspace, dev, stream);
+        case kLeftFp4 * 4 + kRightFp4:
+            return choose_tile<kLeftFp4, kRightFp4>(a, workspace, dev, stream);
+        case kLeftFp4 * 4 + kRightFp8:
+            return choose_tile<kLeftFp4, kRightFp8>(a, workspace, dev, stream);
+        case kLeftFp8 * 4 + kRightFp4:
+            return choose_tile<kLeftFp8, kRightFp4>(a, workspace, dev, stream);
+        case kLeftFp8 * 4 + kRightFp8:
+            return choose_tile<kLeftFp8, kRightFp8>(a, workspace, dev, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace zs_detail

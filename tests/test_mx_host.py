@@ -1,0 +1,261 @@
+"""The microscaled formats' argument checks: the C ABI refuses each bad call with
+its status before anything is enqueued, and the binding refuses tensors that mean
+something else (CPU only: no call gets further than its checks)."""
+import ctypes
+import os
+import re
+import subprocess
+import tempfile
+
+import pytest
+
+import sharded_mixed_precision_shard_amd as zs
+from tests.conftest import ROOT
+
+HEADER = os.path.join(ROOT, "include", "zs.h")
+A, B, C, D, E = (1 << 40, 2 << 40, 3 << 40, 4 << 40, 5 << 40)   # far apart, never touched
+BF16, FP16, FP32 = 0, 1, 2
+FP4, FP8 = 0, 1
+
+
+def matrix(data=A, rows=4, cols=64, ld=None, dtype=BF16, reserved=0):
+    return zs.ZsMatrix(data, rows, cols, cols if ld is None else ld, dtype, reserved)
+
+
+def held(codes=B, scales=C, rows=4, cols=64, fmt=FP4, reserved=0):
+    return zs.ZsMx(codes, scales, rows, cols, fmt, reserved)
+
+
+def ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def quantize(x, q):
+    return zs.load_library().zs_mx_quantize(ref(x), ref(q), None)
+
+
+def dequantize(q, x):
+    return zs.load_library().zs_mx_dequantize(ref(q), ref(x), None)
+
+
+def linear(x=None, w=None, y=None, ws=None):
+    x = matrix(rows=3) if x is None else x
+    w = held(rows=5) if w is None else w
+    y = matrix(D, 3, 5) if y is None else y
+    return zs.load_library().zs_mx_linear(ref(x), ref(w), ref(y), ws, None)
+
+
+def product(x=None, w=None, y=None, ws=None):
+    x = held(A, A + (1 << 30), rows=3) if x is None else x
+    w = held(rows=5) if w is None else w
+    y = matrix(D, 3, 5) if y is None else y
+    return zs.load_library().zs_mx_product(ref(x), ref(w), ref(y), ws, None)
+
+
+def dgrad(dy=None, w=None, dx=None, ws=None):
+    dy = matrix(rows=3, cols=5) if dy is None else dy
+    w = held(rows=5) if w is None else w
+    dx = matrix(D, 3, 64) if dx is None else dx
+    return zs.load_library().zs_mx_linear_dgrad(ref(dy), ref(w), ref(dx), ws, None)
+
+
+def wgrad(dy=None, x=None, dw=None, add=0, ws=None):
+    dy = matrix(rows=3, cols=5) if dy is None else dy
+    x = held(rows=3) if x is None else x
+    dw = matrix(D, 5, 64, dtype=FP32) if dw is None else dw
+    return zs.load_library().zs_mx_linear_wgrad(ref(dy), ref(x), ref(dw), add, ws, None)
+
+
+NOT_READY, INVALID, MISALIGNED, ALIASING = (zs.ZS_ERR_NOT_INITIALIZED, zs.ZS_ERR_INVALID_ARGUMENT,
+                                            zs.ZS_ERR_MISALIGNED, zs.ZS_ERR_ALIASING)
+
+
+@pytest.fixture(autouse=True)
+def not_ready():
+    zs.zs_fini()     # every good call below ends here, at the state of the library
+
+
+def test_good_calls_reach_the_state_of_the_library():
+    for dtype in (BF16, FP16, FP32):
+        for fmt in (FP4, FP8):
+            assert quantize(matrix(dtype=dtype), held(fmt=fmt)) == NOT_READY
+            assert dequantize(held(fmt=fmt), matrix(dtype=dtype)) == NOT_READY
+    for call in (linear, product, dgrad, wgrad):
+        assert call() == NOT_READY
+        assert call(ws=E) == NOT_READY
+    assert wgrad(add=1) == NOT_READY
+    # element alignment and odd strides are enough for matrices, one byte for scales
+    assert quantize(matrix(A + 2, ld=65), held(scales=C + 1)) == NOT_READY
+    assert linear(x=matrix(A + 2, 3, ld=67)) == NOT_READY
+    # empty matrices need no memory
+    assert quantize(matrix(None, 0), held(None, None, 0)) == NOT_READY
+    assert quantize(matrix(None, 4, 0), held(None, None, 4, 0)) == NOT_READY
+    assert linear(x=matrix(None, 3, 0), w=held(None, None, 5, 0)) == NOT_READY
+
+
+CASTS = [
+    (None, held(), INVALID), (matrix(), None, INVALID),
+    (matrix(None), held(), INVALID), (matrix(), held(None), INVALID),
+    (matrix(), held(scales=None), INVALID),
+    (matrix(rows=-1), held(rows=-1), INVALID), (matrix(cols=-1, ld=0), held(cols=-1), INVALID),
+    (matrix(ld=63), held(), INVALID), (matrix(dtype=3), held(), INVALID),
+    (matrix(dtype=-1), held(), INVALID), (matrix(reserved=1), held(), INVALID),
+    (matrix(), held(reserved=1), INVALID), (matrix(), held(fmt=2), INVALID),
+    (matrix(), held(fmt=-1), INVALID), (matrix(rows=5), held(), INVALID),
+    (matrix(cols=65), held(), INVALID),
+    (matrix(A + 1), held(), MISALIGNED), (matrix(A + 2, dtype=FP32), held(), MISALIGNED),
+    (matrix(), held(B + 8), MISALIGNED),
+    (matrix(), held(A), ALIASING), (matrix(), held(A + 4 * 64 * 2 - 16), ALIASING),
+    (matrix(), held(scales=A + 1), ALIASING),
+    # sizes whose bytes no address space holds, and more blocks than one call takes
+    (matrix(rows=1 << 40, cols=1 << 40), held(rows=1 << 40, cols=1 << 40), INVALID),
+    (matrix(rows=1 << 62, cols=1), held(rows=1 << 62, cols=1), INVALID),
+    (matrix(rows=2, ld=1 << 62), held(rows=2), INVALID),
+    (matrix((1 << 64) - 64, rows=4), held(), INVALID),
+    (matrix(rows=1, cols=1 << 38, dtype=BF16), held(rows=1, cols=1 << 38), INVALID),
+]
+
+
+@pytest.mark.parametrize("n", range(len(CASTS)))
+def test_casts_refuse(n):
+    x, q, status = CASTS[n]
+    assert quantize(x, q) == status
+    assert dequantize(q, x) == status
+
+
+def test_quantise_refuses_codes_over_scales():
+    assert quantize(matrix(), held(scales=B + 10)) == ALIASING
+    assert quantize(matrix(), held(scales=B + 4 * 32)) == NOT_READY    # side by side
+
+
+def test_products_refuse():
+    big = 1 << 28
+    for got, status in (
+            (linear(x=matrix(rows=3, dtype=FP16)), INVALID),
+            (linear(x=matrix(rows=3, dtype=FP32)), INVALID),
+            (linear(y=matrix(D, 3, 5, dtype=FP16)), INVALID),
+            (linear(y=matrix(D, 3, 6)), INVALID), (linear(y=matrix(D, 4, 5)), INVALID),
+            (linear(x=matrix(rows=3, cols=65)), INVALID), (linear(w=held(rows=6)), INVALID),
+            (linear(w=held(rows=5, fmt=5)), INVALID), (linear(x=matrix(None, 3)), INVALID),
+            (linear(w=held(None, rows=5)), INVALID), (linear(y=matrix(None, 3, 5)), INVALID),
+            (linear(y=matrix(D, 3, 5, ld=4)), INVALID),
+            (linear(w=held(B + 4, rows=5)), MISALIGNED),
+            (linear(x=matrix(A + 1, 3)), MISALIGNED), (linear(y=matrix(D + 1, 3, 5)), MISALIGNED),
+            (linear(y=matrix(A, 3, 5)), ALIASING), (linear(y=matrix(B, 3, 5)), ALIASING),
+            (linear(y=matrix(C, 3, 5)), ALIASING),
+            (linear(ws=E + 8), MISALIGNED), (linear(ws=A), ALIASING), (linear(ws=B), ALIASING),
+            (linear(ws=C), ALIASING), (linear(ws=D), ALIASING),
+            (linear(ws=D - zs.ZS_MX_WORKSPACE_BYTES + 16), ALIASING),
+            (linear(ws=(1 << 64) - 16), INVALID),
+            (linear(x=matrix(rows=big + 1), y=matrix(D, big + 1, 5)), INVALID),
+            (linear(w=held(rows=big + 1), y=matrix(D, 3, big + 1)), INVALID),
+            (linear(x=matrix(rows=1, cols=big + 1), w=held(rows=1, cols=big + 1),
+                    y=matrix(D, 1, 1)), INVALID),
+            (linear(x=matrix(rows=1 << 20), w=held(rows=1 << 17), y=matrix(D, 1 << 20, 1 << 17)),
+             INVALID),
+            (product(x=held(A, A + (1 << 30), rows=3, cols=65)), INVALID),
+            (product(x=held(A, A + (1 << 30), rows=3, fmt=2)), INVALID),
+            (product(y=matrix(A, 3, 5)), ALIASING),
+            (product(y=matrix(A + (1 << 30), 3, 5)), ALIASING),
+            (product(ws=A + (1 << 30)), ALIASING),
+            (dgrad(dx=matrix(D, 3, 65)), INVALID), (dgrad(dy=matrix(rows=3, cols=6)), INVALID),
+            (dgrad(dy=matrix(rows=3, cols=5, dtype=FP32)), INVALID),
+            (dgrad(dx=matrix(A, 3, 64)), ALIASING),
+            (wgrad(add=2), INVALID), (wgrad(add=-1), INVALID),
+            (wgrad(add=1, dw=matrix(D, 5, 64)), INVALID),       # bf16 is not added to
+            (wgrad(dw=matrix(D, 64, 5, dtype=FP32)), INVALID),
+            (wgrad(x=held(rows=4)), INVALID), (wgrad(dw=matrix(B, 5, 64, dtype=FP32)), ALIASING)):
+        assert got == status
+    lib, x, w, y = zs.load_library(), ref(matrix()), ref(held()), ref(matrix(D))
+    assert lib.zs_mx_product(None, w, y, None, None) == INVALID
+    assert lib.zs_mx_linear(None, w, y, None, None) == INVALID
+    assert lib.zs_mx_linear(x, None, y, None, None) == INVALID
+    assert lib.zs_mx_linear(x, w, None, None, None) == INVALID
+
+
+def test_constants_and_structs_match_the_header():
+    text = open(HEADER).read()
+    for name in ("ZS_MX_BLOCK", "ZS_MX_WORKSPACE_BYTES"):
+        assert int(re.search(r"#define %s (\d+)" % name, text).group(1)) == getattr(zs, name)
+    src = r'''
+    #include <stddef.h>
+    #include <stdio.h>
+    #include "zs.h"
+    int main(void) {
+      printf("%zu %zu %zu %zu %zu %zu %d %d\n", sizeof(zs_mx), offsetof(zs_mx, cols),
+             offsetof(zs_mx, format), sizeof(zs_matrix), offsetof(zs_matrix, ld),
+             offsetof(zs_matrix, dtype), ZS_MX_FP4, ZS_MX_FP8);
+      for (int c = 0; c < 100; ++c)
+        printf("%lld %lld\n", (long long)ZS_MX_ROW_BYTES(ZS_MX_FP4, c),
+               (long long)ZS_MX_ROW_BYTES(ZS_MX_FP8, c));
+      return 0; }
+    '''
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "probe.c"), os.path.join(d, "probe")
+        open(c, "w").write(src)
+        subprocess.run(["gcc", "-std=c99", "-I", os.path.dirname(HEADER), "-o", exe, c],
+                       check=True)
+        got = [int(x) for x in subprocess.run([exe], capture_output=True, text=True,
+                                              check=True).stdout.split()]
+    assert got[:8] == [ctypes.sizeof(zs.ZsMx), zs.ZsMx.cols.offset, zs.ZsMx.format.offset,
+                       ctypes.sizeof(zs.ZsMatrix), zs.ZsMatrix.ld.offset,
+                       zs.ZsMatrix.dtype.offset, zs.ZS_MX_FORMAT["fp4"], zs.ZS_MX_FORMAT["fp8"]]
+    want = [zs.mx_row_bytes(f, c) for c in range(100) for f in ("fp4", "fp8")]
+    assert got[8:] == want
+
+
+def test_binding_refuses():
+    torch = pytest.importorskip("torch")
+    u8 = torch.zeros(4, 32, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="fp4"):
+        zs.Mx(u8, u8, 64, "int4")
+    with pytest.raises(ValueError, match="fp4"):
+        zs.Mx.empty(1, 1, "e4m3", "cpu")
+    with pytest.raises(TypeError, match="codes"):
+        zs.Mx(u8.float(), u8[:, :2], 64, "fp4")
+    with pytest.raises(TypeError, match="scales"):
+        zs.Mx(u8, u8[:, :2].float(), 64, "fp4")
+    with pytest.raises(ValueError, match="no whole rows"):
+        zs.Mx(u8, u8[:, :3].contiguous(), 64, "fp4")
+    with pytest.raises(ValueError, match="negative"):
+        zs.Mx(u8, u8, -1, "fp4")
+    with pytest.raises(ValueError, match="GPU tensor"):      # host memory
+        zs.Mx(u8, u8[:, :2].contiguous(), 64, "fp4")
+    with pytest.raises(ValueError, match="GPU tensor"):
+        zs.zs_mx_quantize(torch.zeros(4, 64), None)
+
+
+class FakeMatrix:
+    """A tensor's questions, on a device that is never touched."""
+    is_cuda = True
+    device = None
+
+    def __init__(self, shape, strides, dtype="torch.bfloat16"):
+        self.shape, self._s, self.dtype = shape, strides, dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return self._s if i is None else self._s[i]
+
+    def data_ptr(self):
+        return A
+
+
+def test_matrices_of_tensors():
+    m = zs._matrix(FakeMatrix((3, 5), (9, 1)), "x")
+    assert (m.rows, m.cols, m.ld, m.dtype) == (3, 5, 9, 0)
+    m = zs._matrix(FakeMatrix((7,), (1,), "torch.float32"), "x")
+    assert (m.rows, m.cols, m.ld, m.dtype) == (1, 7, 7, 2)
+    m = zs._matrix(FakeMatrix((1, 5), (1, 1), "torch.int16"), "x")      # one row: any stride
+    assert (m.rows, m.cols, m.ld, m.dtype) == (1, 5, 5, 0)
+    m = zs._matrix(FakeMatrix((4, 1), (6, 3), "torch.float16"), "x")    # one column: any step
+    assert (m.rows, m.cols, m.ld, m.dtype) == (4, 1, 6, 1)
+    for shape, strides in (((3, 5), (1, 3)), ((3, 5), (4, 1)), ((3, 5), (0, 1)), ((5,), (2,))):
+        with pytest.raises(ValueError, match="side by side"):
+            zs._matrix(FakeMatrix(shape, strides), "x")
+    with pytest.raises(ValueError, match="dimensions"):
+        zs._matrix(FakeMatrix((2, 3, 4), (12, 4, 1)), "x")
+    with pytest.raises(TypeError, match="not bfloat16"):
+        zs._matrix(FakeMatrix((3, 5), (5, 1), "torch.float64"), "x")
