@@ -23,6 +23,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Vectors at any address that suits their elements.
 struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
@@ -44,6 +45,11 @@ __device__ __forceinline__ u32x4 widen_fp8(uint32_t w0, uint32_t w1, float s) {
                  bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true)),
                  bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false)),
                  bits(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true))};
+}
+
+// 32 fp4 codes as an operand of the scaled matrix instruction, which reads four words.
+__device__ __forceinline__ i32x8 codes4(u32x4 v) {
+    return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
 // ------------------------------------------------ quantisation, dequantisation
@@ -431,6 +437,71 @@ __device__ __forceinline__ bool last_split(uint32_t *counter, int splits, uint32
     return last;
 }
 
+// Which tile a workgroup makes.  Workgroups are dealt to the XCDs in turn: each XCD
+// gets a run of neighbouring tiles, and walks it in bands of kBand tiles of i, so that
+// the rows its compute units read at a time are few enough for its L2.
+constexpr int kXcds = 8;
+constexpr int kBand = 8;
+__device__ __forceinline__ void tile_of(int64_t block, int tiles_i, int tiles_j, int *i, int *j) {
+    const int64_t tiles = (int64_t)tiles_i * tiles_j;
+    const int64_t each = tiles / kXcds, more = tiles % kXcds, x = block % kXcds;
+    const int64_t id = x * each + (x < more ? x : more) + block / kXcds;
+    const int64_t band = id / ((int64_t)kBand * tiles_j);
+    const int rows = min(kBand, tiles_i - (int)band * kBand);
+    const int64_t in = id - band * kBand * tiles_j;
+    *i = (int)band * kBand + (int)(in % rows);
+    *j = (int)(in / rows);
+}
+
+// The end of a tile: its sums go out, or to the workspace, where the last of the splits
+// adds them.
+template <int BI, int BJ, int WI, int WJ>
+__device__ __forceinline__ void finish_tile(const MxProductArgs &a,
+                                            const f32x16 (&acc)[BJ / WJ / 32][BI / WI / 32],
+                                            int tile, int split, int i0, int j0, int wi, int wj,
+                                            int wave, int lane, uint32_t *shared) {
+    constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
+    // lane: i = lane % 32, and for each r four j's from 8 r + 4 (lane / 32)
+    const int li = wi + lane % 32, lj = wj + lane / 32 * 4;
+    if (a.splits > 1) {
+        float *mine = a.parts + ((int64_t)tile * a.splits + split) * (BI * BJ);
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    *(f32x4 *)(mine + (((wave * FJ + j) * FI + i) * 4 + r) * 256 + lane * 4) =
+                        f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
+                              acc[j][i][4 * r + 3]};
+        if (!last_split(a.counters + tile, a.splits, shared)) return;
+        const float *parts = a.parts + (int64_t)tile * a.splits * (BI * BJ);
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float *at =
+                        parts + (((wave * FJ + j) * FI + i) * 4 + r) * 256 + lane * 4;
+                    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+                    for (int k = 0; k < a.splits; ++k)  // always in this order
+                        v += *(const f32x4 *)(at + (int64_t)k * (BI * BJ));
+                    put4(a, i0 + li + 32 * i, j0 + lj + 32 * j + 8 * r, v);
+                }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                put4(a, i0 + li + 32 * i, j0 + lj + 32 * j + 8 * r,
+                     f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
+                           acc[j][i][4 * r + 3]});
+}
+
 // A workgroup makes a BI x BJ tile of out (of one split of c).  The matrix
 // instruction takes Q's rows as its rows and P's as its columns: a lane then
 // holds four neighbouring j's of one i, and stores them together.
@@ -444,8 +515,10 @@ __global__ __launch_bounds__(WI *WJ *kWave) void mx_tile(MxProductArgs a) {
     __shared__ __attribute__((aligned(128))) char lds[2 * (P_BYTES + Q_BYTES)];
 
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-    const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-    const int i0 = tile % a.tiles_i * BI, j0 = tile / a.tiles_i * BJ;
+    const int split = blockIdx.x % a.splits;
+    int ti, tj;
+    tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
+    const int tile = tj * a.tiles_i + ti, i0 = ti * BI, j0 = tj * BJ;
     const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
     const int first = split * a.split_steps;
     const int steps = min((a.C + kStep - 1) / kStep - first, a.split_steps);
@@ -502,68 +575,206 @@ __global__ __launch_bounds__(WI *WJ *kWave) void mx_tile(MxProductArgs a) {
         if (more) store((step + 1) % 2);
     }
 
-    // lane: i = lane % 32, and for each r four j's from 8 r + 4 (lane / 32)
-    const int li = wi + lane % 32, lj = wj + lane / 32 * 4;
-    if (a.splits > 1) {
-        float *mine = a.parts + ((int64_t)tile * a.splits + split) * (BI * BJ);
+    finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, (uint32_t *)lds);
+}
+
+// ---------------------------------------------- products of two fp4 operands
+
+// Rows of a tile through LDS as they are stored: kStep4 codes (128 bytes, eight
+// blocks) of each row per step, the chunks of a row permuted by the row's number as
+// at_rows does, and its eight scales beside them.
+constexpr int kStep4 = 256;
+constexpr int kStep4Blocks = kStep4 / kMxBlock;
+
+typedef __attribute__((address_space(3))) void lds_void;
+struct __attribute__((packed, aligned(1))) Bytes8 { uint64_t v; };
+
+// From memory to LDS past the registers: lane l's 16 bytes go to lds + 16 l.  Reads
+// past the buffer's size give zeros; kNowhere, and what is added to it, is past every size.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
+}
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t from, char *lds, uint32_t offset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)lds, 16, (int)offset, 0, 0, 0);
+}
+__device__ __forceinline__ void dma_done() {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Both operands' codes go into the scaled matrix instruction as they are: 64 products
+// of a row and a column per instruction, at four times the rate of bf16.  A lane holds
+// a block of 32, so its scale is one byte, taken from a word of four by number.
+template <int BI, int BJ, int WI, int WJ>
+__global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_fp4(MxProductArgs a) {
+    constexpr int NT = WI * WJ * kWave;
+    constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
+    constexpr int P_BYTES = BI * 128, Q_BYTES = BJ * 128;
+    constexpr int EACH_P = BI * 8 / NT, EACH_Q = BJ * 8 / NT;
+    // two stages, each an array of its own: the compiler sees that what is read of one
+    // does not wait for what is on its way into the other
+    __shared__ __attribute__((aligned(128))) char lds0[P_BYTES + Q_BYTES];
+    __shared__ __attribute__((aligned(128))) char lds1[P_BYTES + Q_BYTES];
+    __shared__ uint64_t scales0[NT];
+    __shared__ uint64_t scales1[NT];
+
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int split = blockIdx.x % a.splits;
+    int ti, tj;
+    tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
+    const int tile = tj * a.tiles_i + ti, i0 = ti * BI, j0 = tj * BJ;
+    const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+    const int nb = (int)a.q.nb;
+    const uint32_t row_bytes = (uint32_t)nb * 16u;
+    const int first = split * a.split_steps;
+    const int steps = min((nb + kStep4Blocks - 1) / kStep4Blocks - first, a.split_steps);
+
+    const auto p_buf = buffer_of(a.px.codes + (int64_t)i0 * row_bytes,
+                                 (uint32_t)min(a.I - i0, BI) * row_bytes);
+    const auto q_buf = buffer_of(a.q.codes + (int64_t)j0 * row_bytes,
+                                 (uint32_t)min(a.J - j0, BJ) * row_bytes);
+    // a wave's chunk k: eight rows, lane / 8 the row, lane % 8 the place in it
+    const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row & 7);
+    const uint32_t p_off = (uint32_t)row * row_bytes + (uint32_t)chunk * 16u;
+    static_assert(NT >= BI + BJ, "a thread for the scales of each row");
+    const uint8_t *my_scales =
+        tid < BI ? a.px.scales + (int64_t)min(i0 + tid, a.I - 1) * nb
+                 : a.q.scales + (int64_t)min(j0 + tid - BI, a.J - 1) * nb;
+
+    auto fetch = [&](char *lds, int step) {
+        const int block = (first + step) * kStep4Blocks;
+        // blocks past the row's end read as zero codes (all of the address is in the lane's
+        // offset, which is what the size is compared with)
+        const uint32_t off = block + chunk < nb ? p_off + (uint32_t)block * 16u : kNowhere;
 #pragma unroll
-        for (int j = 0; j < FJ; ++j)
+        for (int k = 0; k < EACH_P; ++k)
+            dma16(p_buf, lds + (k * (NT / 8) + wave * 8) * 128,
+                  off + (uint32_t)(k * (NT / 8)) * row_bytes);
 #pragma unroll
-            for (int i = 0; i < FI; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    *(f32x4 *)(mine + (((wave * FJ + j) * FI + i) * 4 + r) * 256 + lane * 4) =
-                        f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
-                              acc[j][i][4 * r + 3]};
-        if (!last_split(a.counters + tile, a.splits, (uint32_t *)lds)) return;
-        const float *parts = a.parts + (int64_t)tile * a.splits * (BI * BJ);
-#pragma unroll
-        for (int j = 0; j < FJ; ++j)
-#pragma unroll
-            for (int i = 0; i < FI; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float *at =
-                        parts + (((wave * FJ + j) * FI + i) * 4 + r) * 256 + lane * 4;
-                    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int k = 0; k < a.splits; ++k)  // always in this order
-                        v += *(const f32x4 *)(at + (int64_t)k * (BI * BJ));
-                    put4(a, i0 + li + 32 * i, j0 + lj + 32 * j + 8 * r, v);
-                }
-        return;
-    }
+        for (int k = 0; k < EACH_Q; ++k)
+            dma16(q_buf, lds + P_BYTES + (k * (NT / 8) + wave * 8) * 128,
+                  off + (uint32_t)(k * (NT / 8)) * row_bytes);
+    };
+    // eight bytes inside the row, shifted where they reach back: what is past the row's
+    // end becomes 0 or 1, scales of zero codes.  No branch: one here would cost registers
+    // that the sums need.
+    auto fetch_scales = [&](int step) -> uint64_t {
+        const int block = (first + step) * kStep4Blocks;
+        const int from = min(block, nb - kStep4Blocks);
+        return ((const Bytes8 *)(my_scales + from))->v >> min(8 * (block - from), 63);
+    };
+
+    f32x16 acc[FJ][FI];
 #pragma unroll
     for (int j = 0; j < FJ; ++j)
 #pragma unroll
-        for (int i = 0; i < FI; ++i)
+        for (int i = 0; i < FI; ++i) acc[j][i] = f32x16{};
+
+    const int r = lane % 32, h = lane / 32;
+    auto multiply = [&](const char *lds, const uint64_t *scales) {
+        const char *p = lds + (wi + r) * 128, *q = lds + P_BYTES + (wj + r) * 128;
+        uint32_t ps[FI], qs[FJ];
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                put4(a, i0 + li + 32 * i, j0 + lj + 32 * j + 8 * r,
-                     f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
-                           acc[j][i][4 * r + 3]});
+        for (int i = 0; i < FI; ++i) ps[i] = ((const uint32_t *)(scales + wi + 32 * i + r))[h];
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) qs[j] = ((const uint32_t *)(scales + BI + wj + 32 * j + r))[h];
+        // the four blocks of a lane's half row; the number of the scale is part of the
+        // instruction
+#define ZS_MX_QUARTER(S)                                                                       \
+    {                                                                                          \
+        const int at = ((4 * h + S) ^ (r & 7)) << 4;                                           \
+        i32x8 pf[FI], qf[FJ];                                                                  \
+        _Pragma("unroll") for (int i = 0; i < FI; ++i) pf[i] =                                 \
+            codes4(*(const u32x4 *)(p + i * 4096 + at));                                       \
+        _Pragma("unroll") for (int j = 0; j < FJ; ++j) qf[j] =                                 \
+            codes4(*(const u32x4 *)(q + j * 4096 + at));                                       \
+        _Pragma("unroll") for (int j = 0; j < FJ; ++j) _Pragma("unroll") for (int i = 0; i < FI; \
+                                                                              ++i) acc[j][i] = \
+            __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(qf[j], pf[i], acc[j][i], 4, 4, S,  \
+                                                            (int)qs[j], S, (int)ps[i]);        \
+    }
+        ZS_MX_QUARTER(0)
+        ZS_MX_QUARTER(1)
+        ZS_MX_QUARTER(2)
+        ZS_MX_QUARTER(3)
+#undef ZS_MX_QUARTER
+    };
+
+    if (steps > 0) {
+        fetch(lds0, 0);
+        scales0[tid] = fetch_scales(0);
+    }
+    // two steps a turn: a split ends with a whole turn, or with the row, past which all is 0
+#pragma unroll 1
+    for (int step = 0; step < steps; step += 2) {
+        dma_done();
+        __syncthreads();
+        fetch(lds1, step + 1);
+        uint64_t s = fetch_scales(step + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(lds0, scales0);
+        scales1[tid] = s;
+        dma_done();
+        __syncthreads();
+        fetch(lds0, step + 2);
+        s = fetch_scales(step + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(lds1, scales1);
+        scales0[tid] = s;
+    }
+    finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
+                                (uint32_t *)scales1);
 }
 
-template <int BI, int BJ, int WI, int WJ, int LEFT, int RIGHT>
-hipError_t run_tile(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    a.tiles_i = (a.I + BI - 1) / BI;
-    a.tiles_j = (a.J + BJ - 1) / BJ;
-    const int64_t tiles = (int64_t)a.tiles_i * a.tiles_j;
-    const int steps = (a.C + kStep - 1) / kStep;
+// Tiles of out and splits of c for a kernel of bi x bj tiles whose steps take `depth` c's
+// and whose splits are whole turns of `turn` steps.
+void plan(MxProductArgs *a, int bi, int bj, int depth, int turn, void *workspace,
+          const MxDevice &dev) {
+    a->tiles_i = (a->I + bi - 1) / bi;
+    a->tiles_j = (a->J + bj - 1) / bj;
+    const int64_t tiles = (int64_t)a->tiles_i * a->tiles_j;
+    const int steps = (a->C + depth - 1) / depth;
     int64_t splits = 1;
     if (workspace && tiles <= kMxCounters && tiles < dev.cus) {
         splits = dev.cus / tiles;
         splits = splits < steps / 8 ? splits : steps / 8;
-        const int64_t room = kMxPartBytes / (tiles * BI * BJ * 4);
+        const int64_t room = kMxPartBytes / (tiles * bi * bj * 4);
         splits = splits < room ? splits : room;
         splits = splits > 1 ? splits : 1;
     }
-    a.split_steps = steps > 0 ? (int)((steps + splits - 1) / splits) : 0;
-    a.splits = steps > 0 ? (steps + a.split_steps - 1) / a.split_steps : 1;
-    a.counters = (uint32_t *)workspace;
-    a.parts = (float *)((char *)workspace + kMxCounterBytes);
-    mx_tile<BI, BJ, WI, WJ, LEFT, RIGHT>
-        <<<dim3((uint32_t)(tiles * a.splits)), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    a->split_steps = steps > 0 ? (int)((steps + splits - 1) / splits + turn - 1) / turn * turn : 0;
+    a->splits = steps > 0 ? (steps + a->split_steps - 1) / a->split_steps : 1;
+    a->counters = (uint32_t *)workspace;
+    a->parts = (float *)((char *)workspace + kMxCounterBytes);
+}
+
+dim3 grid_of(const MxProductArgs &a) {
+    return dim3((uint32_t)((int64_t)a.tiles_i * a.tiles_j * a.splits));
+}
+
+template <int BI, int BJ, int WI, int WJ, int LEFT, int RIGHT>
+hipError_t run_tile(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
+    plan(&a, BI, BJ, kStep, 1, workspace, dev);
+    mx_tile<BI, BJ, WI, WJ, LEFT, RIGHT><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
     return hipGetLastError();
+}
+
+template <int BI, int BJ, int WI, int WJ>
+hipError_t run_fp4(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
+    plan(&a, BI, BJ, kStep4, 2, workspace, dev);
+    mx_tile_fp4<BI, BJ, WI, WJ><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &dev,
+                      hipStream_t stream) {
+    const int64_t out = (int64_t)a.I * a.J;
+    if (out >= (int64_t)dev.cus * 256 * 256)
+        return run_fp4<256, 256, 2, 4>(a, workspace, dev, stream);
+    if (out >= (int64_t)dev.cus * 128 * 128)
+        return run_fp4<128, 128, 2, 2>(a, workspace, dev, stream);
+    return run_fp4<64, 64, 2, 2>(a, workspace, dev, stream);
 }
 
 template <int LEFT, int RIGHT>
@@ -626,6 +837,9 @@ hipError_t launch_mx_product(MxLeft left, int right, MxProductArgs a, void *work
         case kLeftCols * 4 + c4: return choose_tile<kLeftCols, c4>(a, workspace, dev, stream);
         case kLeftCols * 4 + c8: return choose_tile<kLeftCols, c8>(a, workspace, dev, stream);
         case kLeftFp4 * 4 + kRightFp4:
+            // offsets inside a tile's rows are 32-bit numbers below kNowhere
+            if (a.q.nb >= kStep4Blocks && a.q.nb * 16 * 256 < (int64_t)kNowhere)
+                return choose_fp4(a, workspace, dev, stream);
             return choose_tile<kLeftFp4, kRightFp4>(a, workspace, dev, stream);
         case kLeftFp4 * 4 + kRightFp8:
             return choose_tile<kLeftFp4, kRightFp8>(a, workspace, dev, stream);
