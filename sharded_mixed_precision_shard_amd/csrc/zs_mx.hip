@@ -598,9 +598,28 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint3
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t from, char *lds, uint32_t offset) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)lds, 16, (int)offset, 0, 0, 0);
 }
-__device__ __forceinline__ void dma_done() {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+// A workgroup's stage is ready: at most N of each wave's memory operations are still on
+// their way (they end in order), and nothing of the stage before is still being read.
+template <int N>
+__device__ __forceinline__ void stage_ready() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
+
+// Eight scales of a row from `block` on, inside the row, shifted where they reach back: what
+// is past the row's end becomes 0 or 1, scales that stand for numbers.  No branch: in the
+// loops below one would cost registers that the sums need.
+struct Scales8 {
+    uint64_t raw;
+    int shift;
+    __device__ __forceinline__ void load(const uint8_t *row, int block, int nb) {
+        const int from = min(block, nb - 8);
+        raw = ((const Bytes8 *)(row + from))->v;
+        shift = min(8 * (block - from), 63);
+    }
+    __device__ __forceinline__ uint64_t value() const { return raw >> shift; }
+};
 
 // Both operands' codes go into the scaled matrix instruction as they are: 64 products
 // of a row and a column per instruction, at four times the rate of bf16.  A lane holds
@@ -656,13 +675,10 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_fp4(MxProductArgs a)
             dma16(q_buf, lds + P_BYTES + (k * (NT / 8) + wave * 8) * 128,
                   off + (uint32_t)(k * (NT / 8)) * row_bytes);
     };
-    // eight bytes inside the row, shifted where they reach back: what is past the row's
-    // end becomes 0 or 1, scales of zero codes.  No branch: one here would cost registers
-    // that the sums need.
-    auto fetch_scales = [&](int step) -> uint64_t {
-        const int block = (first + step) * kStep4Blocks;
-        const int from = min(block, nb - kStep4Blocks);
-        return ((const Bytes8 *)(my_scales + from))->v >> min(8 * (block - from), 63);
+    auto fetch_scales = [&](int step) {
+        Scales8 s;
+        s.load(my_scales, (first + step) * kStep4Blocks, nb);
+        return s;
     };
 
     f32x16 acc[FJ][FI];
@@ -703,28 +719,209 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_fp4(MxProductArgs a)
 
     if (steps > 0) {
         fetch(lds0, 0);
-        scales0[tid] = fetch_scales(0);
+        scales0[tid] = fetch_scales(0).value();
     }
     // two steps a turn: a split ends with a whole turn, or with the row, past which all is 0
 #pragma unroll 1
     for (int step = 0; step < steps; step += 2) {
-        dma_done();
-        __syncthreads();
+        stage_ready<0>();
         fetch(lds1, step + 1);
-        uint64_t s = fetch_scales(step + 1);
+        Scales8 s = fetch_scales(step + 1);
         __builtin_amdgcn_sched_barrier(0);
         multiply(lds0, scales0);
-        scales1[tid] = s;
-        dma_done();
-        __syncthreads();
+        scales1[tid] = s.value();
+        stage_ready<0>();
         fetch(lds0, step + 2);
         s = fetch_scales(step + 2);
         __builtin_amdgcn_sched_barrier(0);
         multiply(lds1, scales1);
-        scales0[tid] = s;
+        scales0[tid] = s.value();
     }
     finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
                                 (uint32_t *)scales1);
+}
+
+// ------------------------------------- bf16 against blocks, rows in full chunks
+
+// A bf16 operand that DMA can take to LDS: rows a multiple of 16 bytes apart, and the
+// rows of a tile (or of a step) inside the reach of a 32-bit offset.
+constexpr int64_t kReach = int64_t(1) << 31;
+
+// y = x w^T.  x goes through LDS by DMA, four steps deep.  w's codes stay packed: a lane
+// loads the block that it multiplies straight into registers, three steps ahead, and
+// widens it there, so LDS carries only x.  Half a wave (32 rows of w) takes one of a
+// step's two blocks, and the four instructions of a step its four words.
+template <int BI, int BJ, int WI, int WJ, bool F8>
+__global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_rows(MxProductArgs a) {
+    constexpr int NT = WI * WJ * kWave;
+    constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
+    constexpr int EACH = BI * 8 / NT;
+    constexpr int W = F8 ? 2 : 1;
+    __shared__ __attribute__((aligned(128))) char lds0[BI * 128];
+    __shared__ __attribute__((aligned(128))) char lds1[BI * 128];
+    __shared__ __attribute__((aligned(128))) char lds2[BI * 128];
+    __shared__ __attribute__((aligned(128))) char lds3[BI * 128];
+
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int split = blockIdx.x % a.splits;
+    int ti, tj;
+    tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
+    const int tile = tj * a.tiles_i + ti, i0 = ti * BI, j0 = tj * BJ;
+    const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+    const int nb = (int)a.q.nb;
+    const int first = split * a.split_steps;
+    const int steps = min((a.C + kStep - 1) / kStep - first, a.split_steps);
+    const int r = lane % 32, h = lane / 32;
+
+    const uint32_t row_bytes = (uint32_t)a.ldp * 2u;
+    const auto p_buf = buffer_of(a.p + (int64_t)i0 * a.ldp, (uint32_t)min(a.I - i0, BI) * row_bytes);
+    const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row & 7);
+    const uint32_t p_off = (uint32_t)row * row_bytes + (uint32_t)chunk * 16u;
+    const uint8_t *codes[FJ];
+    const uint8_t *scales[FJ];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) {
+        const int64_t at = (int64_t)min(j0 + wj + 32 * j + r, a.J - 1) * nb;
+        codes[j] = a.q.codes + at * (16 * W);
+        scales[j] = a.q.scales + at;
+    }
+
+    auto fetch = [&](char *lds, int step) {
+        const int c = (first + step) * kStep;
+        // whole chunks only: the rest of a row is added at the end
+        const uint32_t off = c + chunk * 8 + 8 <= a.C ? p_off + (uint32_t)c * 2u : kNowhere;
+#pragma unroll
+        for (int k = 0; k < EACH; ++k)
+            dma16(p_buf, lds + (k * (NT / 8) + wave * 8) * 128,
+                  off + (uint32_t)(k * (NT / 8)) * row_bytes);
+    };
+    struct Codes {
+        u32x4 v[FJ][W];
+    };
+    auto fetch_codes = [&](int step) {
+        Codes q;
+        const int block = min((first + step) * 2 + h, nb - 1);
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int w = 0; w < W; ++w) q.v[j][w] = ((const u32x4 *)codes[j])[block * W + w];
+        return q;
+    };
+
+    f32x16 acc[FJ][FI];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int i = 0; i < FI; ++i) acc[j][i] = f32x16{};
+
+    auto multiply = [&](const char *lds, const Codes &q, const float (&s)[FJ]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            bf16x8 pf[FI], qf[FJ];
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+                pf[i] = *(const bf16x8 *)(lds + at_rows(wi + 32 * i + r, 4 * h + k));
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) {
+                if constexpr (F8)
+                    qf[j] = __builtin_bit_cast(
+                        bf16x8, widen_fp8(q.v[j][k / 2][k % 2 * 2], q.v[j][k / 2][k % 2 * 2 + 1],
+                                          s[j]));
+                else
+                    qf[j] = __builtin_bit_cast(bf16x8, widen_fp4(q.v[j][0][k], s[j]));
+            }
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int i = 0; i < FI; ++i)
+                    acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[j], pf[i], acc[j][i], 0,
+                                                                        0, 0);
+        }
+    };
+    // what a row holds past its last whole chunk, fewer than 8 elements
+    const int whole = a.C & ~7;
+    if (whole < a.C && split == 0) {
+        const int at = whole % kMxBlock / 8;
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) {
+            const float s = scale_of(scales[j][whole / kMxBlock]);
+            const uint32_t *w =
+                (const uint32_t *)(codes[j] + (int64_t)(whole / kMxBlock) * (16 * W)) + at * W;
+            u32x4 qf = {0, 0, 0, 0};
+            if (h == 0) {
+                if constexpr (F8)
+                    qf = widen_fp8(w[0], w[1], s);
+                else
+                    qf = widen_fp4(w[0], s);
+            }
+#pragma unroll
+            for (int i = 0; i < FI; ++i) {
+                u32x4 pf = {0, 0, 0, 0};
+                const uint16_t *x =
+                    a.p + (int64_t)min(i0 + wi + 32 * i + r, a.I - 1) * a.ldp + whole;
+                if (h == 0)
+                    for (int e = 0; e < a.C - whole; ++e)
+                        pf[e / 2] |= (uint32_t)x[e] << (16 * (e % 2));
+                acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8, qf), __builtin_bit_cast(bf16x8, pf), acc[j][i], 0,
+                    0, 0);
+            }
+        }
+    }
+
+    // the scales of a turn of four steps, and the next
+    uint64_t now[FJ];
+    Scales8 next[FJ];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j) {
+        next[j].load(scales[j], first * 2, nb);
+        now[j] = next[j].value();
+    }
+    // fp8 codes take twice the registers, and are loaded a step later
+    constexpr int FAR = F8 ? 2 : 3;
+    Codes q0, q1, q2, q3;
+    fetch(lds0, 0);
+    q0 = fetch_codes(0);
+    fetch(lds1, 1);
+    q1 = fetch_codes(1);
+    fetch(lds2, 2);
+    if constexpr (FAR > 2) q2 = fetch_codes(2);
+    // Of each step EACH transfers to LDS are followed by FJ * W loads of codes; the
+    // transfers of two steps may be on their way while one is multiplied.
+    constexpr int AHEAD = 2 * EACH + (F8 ? 1 : 2) * FJ * W;
+#define ZS_MX_STEP(T, HERE, Q, NEXT, QN)                                    \
+    {                                                                       \
+        stage_ready<AHEAD>();                                               \
+        fetch(NEXT, step + T + 3);                                          \
+        QN = fetch_codes(step + T + FAR);                                   \
+        __builtin_amdgcn_sched_barrier(0);                                  \
+        float s[FJ];                                                        \
+        _Pragma("unroll") for (int j = 0; j < FJ; ++j) s[j] =               \
+            scale_of((uint32_t)(now[j] >> (16 * T)) >> (8 * h) & 255u);     \
+        multiply(HERE, Q, s);                                               \
+    }
+#pragma unroll 1
+    for (int step = 0; step < steps; step += 4) {
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) next[j].load(scales[j], (first + step) * 2 + 8, nb);
+        if constexpr (F8) {
+            ZS_MX_STEP(0, lds0, q0, lds3, q2)
+            ZS_MX_STEP(1, lds1, q1, lds0, q3)
+            ZS_MX_STEP(2, lds2, q2, lds1, q0)
+            ZS_MX_STEP(3, lds3, q3, lds2, q1)
+        } else {
+            ZS_MX_STEP(0, lds0, q0, lds3, q3)
+            ZS_MX_STEP(1, lds1, q1, lds0, q0)
+            ZS_MX_STEP(2, lds2, q2, lds1, q1)
+            ZS_MX_STEP(3, lds3, q3, lds2, q2)
+        }
+#pragma unroll
+        for (int j = 0; j < FJ; ++j) now[j] = next[j].value();
+    }
+#undef ZS_MX_STEP
+    stage_ready<0>();
+    finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, (uint32_t *)lds0);
 }
 
 // Tiles of out and splits of c for a kernel of bi x bj tiles whose steps take `depth` c's
@@ -765,6 +962,28 @@ hipError_t run_fp4(MxProductArgs a, void *workspace, const MxDevice &dev, hipStr
     plan(&a, BI, BJ, kStep4, 2, workspace, dev);
     mx_tile_fp4<BI, BJ, WI, WJ><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
     return hipGetLastError();
+}
+
+template <int BI, int BJ, int WI, int WJ, bool F8>
+hipError_t run_rows(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
+    plan(&a, BI, BJ, kStep, 4, workspace, dev);
+    mx_tile_rows<BI, BJ, WI, WJ, F8><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+// Whether DMA can take the bf16 operand: 16-byte chunks of its rows at 16-byte addresses,
+// `rows` of them within a 32-bit offset.
+bool dma_takes(const MxProductArgs &a, int64_t rows) {
+    return (uintptr_t)a.p % 16 == 0 && a.ldp % 8 == 0 && a.ldp * 2 * rows < kReach;
+}
+
+template <bool F8>
+hipError_t choose_rows(const MxProductArgs &a, void *workspace, const MxDevice &dev,
+                       hipStream_t stream) {
+    const int64_t out = (int64_t)a.I * a.J;
+    if (out >= (int64_t)dev.cus * 256 * 256)
+        return run_rows<256, 256, 2, 4, F8>(a, workspace, dev, stream);
+    return run_rows<128, 128, 2, 2, F8>(a, workspace, dev, stream);
 }
 
 hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &dev,
@@ -829,8 +1048,12 @@ hipError_t launch_mx_product(MxLeft left, int right, MxProductArgs a, void *work
     constexpr int c4 = kRightFp4 | kRightCols, c8 = kRightFp8 | kRightCols;
     switch (left * 4 + right) {
         case kLeftRows * 4 + kRightFp4:
+            if (a.q.nb >= 8 && dma_takes(a, 256))
+                return choose_rows<false>(a, workspace, dev, stream);
             return choose_tile<kLeftRows, kRightFp4>(a, workspace, dev, stream);
         case kLeftRows * 4 + kRightFp8:
+            if (a.q.nb >= 8 && dma_takes(a, 256))
+                return choose_rows<true>(a, workspace, dev, stream);
             return choose_tile<kLeftRows, kRightFp8>(a, workspace, dev, stream);
         case kLeftRows * 4 + c4: return choose_tile<kLeftRows, c4>(a, workspace, dev, stream);
         case kLeftRows * 4 + c8: return choose_tile<kLeftRows, c8>(a, workspace, dev, stream);

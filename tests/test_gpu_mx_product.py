@@ -379,3 +379,40 @@ def test_linear_gradients_against_differences(gpu):
             diff = (loss(up, other) - loss(down, other)) / 2 if first else \
                 (loss(other, up) - loss(other, down)) / 2
             assert got[i, j] == diff
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+def test_aligned_rows(gpu, workspace, op, fmt):
+    """Rows a multiple of 16 bytes apart, with and without a rest past the last whole chunk
+    (the gaps hold NaN), every number of steps around a turn of the loops."""
+    torch = gpu
+    for n, depth in enumerate((225, 256, 257, 263, 320, 384, 449, 511, 512, 513, 700, 1031, 1279,
+                               2048, 2111)):
+        m, other = [(3, 130), (130, 257), (257, 70), (70, 300)][n % 4]
+        size = {"dgrad": (m, depth, other), "wgrad": (depth, m, other)}.get(op, (m, other, depth))
+        width = m if op == "wgrad" else depth
+        case = Case(torch, op, *size, fmt, True, n, ("fp4", "fp8")[n % 2], -width % 8, 8 * (n % 3))
+        for space in (None, workspace):
+            for kind in (torch.float32, torch.bfloat16):
+                _, out = case.out(kind)
+                case.call(out, space)
+                case.check_equal(out)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("depth", [320, 1300])
+def test_many_tiles(gpu, workspace, op, fmt, depth):
+    """Outputs large enough for the largest tiles, ragged at both ends."""
+    torch = gpu
+    m, other = 4100, 4360
+    size = {"dgrad": (m, depth, other), "wgrad": (depth, m, other)}.get(op, (m, other, depth))
+    case = Case(torch, op, *size, fmt, True, depth, fmt, 4 if op == "wgrad" else 4 * (depth % 8))
+    for kind in (torch.float32, torch.bfloat16):
+        flat, out = case.out(kind, 8)
+        before = flat.clone()
+        case.call(out, workspace)
+        case.check_equal(out)
+        out.fill_(55.0)
+        assert torch.equal(flat, before)
