@@ -419,6 +419,16 @@ __device__ __forceinline__ void put4(const MxProductArgs &a, int i, int j, f32x4
     }
 }
 
+// One value of out.
+__device__ __forceinline__ void put1(const MxProductArgs &a, int i, int j, float v) {
+    if (i >= a.I || j >= a.J) return;
+    const int64_t at = (int64_t)i * a.ldo + j;
+    if (a.out_f32)
+        ((float *)a.out)[at] = v;
+    else
+        ((__bf16 *)a.out)[at] = (__bf16)v;
+}
+
 // Which of a tile's splits arrives last: it finds the others' sums in memory.
 // All threads call it after they have written theirs.
 __device__ __forceinline__ bool last_split(uint32_t *counter, int splits, uint32_t *shared) {
@@ -924,6 +934,241 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_rows(MxProductArgs a
     finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, (uint32_t *)lds0);
 }
 
+// ------------------------------------------------------- products of few rows
+
+// Up to 16 MF rows of x: bound by the bytes of w, which every wave takes 16 NF rows of,
+// 16 blocks (kTurn) at a time, the waves of a workgroup in turn along the row.  Of a turn
+// the lanes of quarter g load the blocks 4 u + g, u = 0 .. 3: 64 neighbouring bytes of a row
+// at a time.  The sums of the waves are joined in LDS, those of the workgroups that share
+// a strip in the workspace.
+constexpr int kTurn = 16;
+
+struct __attribute__((packed, aligned(1))) Bytes16 { u32x4 v; };
+
+template <int LEFT, bool F8, int MF, int NF, int WAVES>
+__global__ __launch_bounds__(WAVES *kWave) void mx_few(MxProductArgs a) {
+    constexpr bool PLAIN = LEFT == kLeftRows, P8 = LEFT == kLeftFp8;
+    constexpr bool SCALED = LEFT == kLeftFp4 && !F8;
+    constexpr int WQ = F8 ? 2 : 1, WP = P8 ? 2 : 1;
+    constexpr int OUT = NF * 16 * MF * 16;
+    __shared__ float sums[WAVES][OUT];
+    __shared__ uint32_t shared;
+
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int strip = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+    const int j0 = strip * (NF * 16);
+    const int r = lane % 16, g = lane / 16;
+    const int nb = (int)a.q.nb;
+    const int turns = min((nb + kTurn - 1) / kTurn, (split + 1) * a.split_steps);
+
+    const uint8_t *q_codes[NF], *q_scales[NF];
+#pragma unroll
+    for (int n = 0; n < NF; ++n) {
+        const int64_t at = (int64_t)min(j0 + 16 * n + r, a.J - 1) * nb;
+        q_codes[n] = a.q.codes + at * (16 * WQ);
+        q_scales[n] = a.q.scales + at;
+    }
+    const uint16_t *p_rows[MF];
+    const uint8_t *p_codes[MF], *p_scales[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+        const int64_t row = min(16 * m + r, a.I - 1);
+        p_rows[m] = a.p + row * a.ldp;
+        p_codes[m] = a.px.codes + row * nb * (16 * WP);
+        p_scales[m] = a.px.scales + row * nb;
+    }
+
+    f32x4 acc[NF][MF];
+#pragma unroll
+    for (int n = 0; n < NF; ++n)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) acc[n][m] = f32x4{};
+
+    struct Blocks {
+        u32x4 code[NF][4][WQ];
+        u32x4 scale[NF];
+    };
+    // the blocks of a turn that lies inside the row
+    auto fetch = [&](int turn) {
+        Blocks b;
+#pragma unroll
+        for (int n = 0; n < NF; ++n) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int w = 0; w < WQ; ++w)
+                    b.code[n][u][w] =
+                        ((const u32x4 *)q_codes[n])[(turn * kTurn + 4 * u + g) * WQ + w];
+            b.scale[n] = ((const Bytes16 *)(q_scales[n] + turn * kTurn))->v;
+        }
+        return b;
+    };
+    // one block of every row: q's codes, and the block of x, whose scale is ps
+    auto multiply = [&](const u32x4 (&code)[NF][WQ], const uint32_t (&qs)[NF],
+                        const u32x4 (&pv)[MF][PLAIN ? 4 : WP], const uint32_t (&ps)[MF]) {
+        if constexpr (SCALED) {
+#pragma unroll
+            for (int n = 0; n < NF; ++n)
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+                    acc[n][m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        codes4(code[n][0]), codes4(pv[m][0]), acc[n][m], 4, 4, 0, (int)qs[n], 0,
+                        (int)ps[m]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                bf16x8 qf[NF], pf[MF];
+#pragma unroll
+                for (int n = 0; n < NF; ++n) {
+                    const float s = scale_of(qs[n]);
+                    if constexpr (F8)
+                        qf[n] = __builtin_bit_cast(
+                            bf16x8, widen_fp8(code[n][k / 2][k % 2 * 2],
+                                              code[n][k / 2][k % 2 * 2 + 1], s));
+                    else
+                        qf[n] = __builtin_bit_cast(bf16x8, widen_fp4(code[n][0][k], s));
+                }
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    const float s = scale_of(ps[m]);
+                    if constexpr (PLAIN)
+                        pf[m] = __builtin_bit_cast(bf16x8, pv[m][k]);
+                    else if constexpr (P8)
+                        pf[m] = __builtin_bit_cast(
+                            bf16x8,
+                            widen_fp8(pv[m][k / 2][k % 2 * 2], pv[m][k / 2][k % 2 * 2 + 1], s));
+                    else
+                        pf[m] = __builtin_bit_cast(bf16x8, widen_fp4(pv[m][0][k], s));
+                }
+#pragma unroll
+                for (int n = 0; n < NF; ++n)
+#pragma unroll
+                    for (int m = 0; m < MF; ++m)
+                        acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(qf[n], pf[m],
+                                                                            acc[n][m], 0, 0, 0);
+            }
+        }
+    };
+
+    // turns inside the row, the next one's blocks on their way while one is multiplied
+    const int inside = min(turns, (PLAIN ? a.C / kMxBlock : nb) / kTurn);
+    int turn = split * a.split_steps + wave;
+    if (turn < inside) {
+        Blocks now = fetch(turn);
+        while (true) {
+            const bool more = turn + WAVES < inside;
+            Blocks next;
+            if (more) next = fetch(turn + WAVES);
+            u32x4 xs[MF];
+            if constexpr (!PLAIN) {
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+                    xs[m] = ((const Bytes16 *)(p_scales[m] + turn * kTurn))->v;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int block = turn * kTurn + 4 * u + g;
+                u32x4 pv[MF][PLAIN ? 4 : WP], code[NF][WQ];
+                uint32_t qs[NF], ps[MF];
+#pragma unroll
+                for (int m = 0; m < MF; ++m) {
+                    ps[m] = 127;
+                    if constexpr (PLAIN) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            pv[m][k] =
+                                ((const Any16 *)(p_rows[m] + (int64_t)block * kMxBlock))[k].v;
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < WP; ++w)
+                            pv[m][w] = ((const u32x4 *)p_codes[m])[block * WP + w];
+                        ps[m] = xs[m][u] >> (8 * g) & 255u;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NF; ++n) {
+#pragma unroll
+                    for (int w = 0; w < WQ; ++w) code[n][w] = now.code[n][u][w];
+                    qs[n] = now.scale[n][u] >> (8 * g) & 255u;
+                }
+                multiply(code, qs, pv, ps);
+            }
+            if (!more) break;
+            turn += WAVES;
+            now = next;
+        }
+        turn += WAVES;
+    }
+    // turns that the row ends in, block by block and element by element
+    for (; turn < turns; turn += WAVES)
+        for (int u = 0; u < 4 && turn * kTurn + 4 * u < nb; ++u) {
+            const int block = turn * kTurn + 4 * u + g;
+            const bool in = block < nb;
+            u32x4 pv[MF][PLAIN ? 4 : WP], code[NF][WQ];
+            uint32_t qs[NF], ps[MF];
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                ps[m] = 127;
+                if constexpr (PLAIN) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int c = block * kMxBlock + 8 * k;
+                        pv[m][k] = u32x4{0, 0, 0, 0};
+                        if (c + 8 <= a.C)
+                            pv[m][k] = ((const Any16 *)(p_rows[m] + c))->v;
+                        else
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                if (c + e < a.C)
+                                    pv[m][k][e / 2] |= (uint32_t)p_rows[m][c + e] << (16 * (e % 2));
+                    }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < WP; ++w)
+                        pv[m][w] = in ? ((const u32x4 *)p_codes[m])[block * WP + w]
+                                      : u32x4{0, 0, 0, 0};
+                    if (in) ps[m] = p_scales[m][block];
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+#pragma unroll
+                for (int w = 0; w < WQ; ++w)
+                    code[n][w] = in ? ((const u32x4 *)q_codes[n])[block * WQ + w]
+                                    : u32x4{0, 0, 0, 0};
+                qs[n] = in ? q_scales[n][block] : 127;
+            }
+            multiply(code, qs, pv, ps);
+        }
+
+    // lane: i = lane % 16, four j's from 4 (lane / 16)
+#pragma unroll
+    for (int n = 0; n < NF; ++n)
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+            *(f32x4 *)&sums[wave][(m * 16 + r) * (NF * 16) + n * 16 + 4 * g] = acc[n][m];
+    __syncthreads();
+    float *mine = a.parts + ((int64_t)strip * a.splits + split) * OUT;
+    const int rows = min(a.I, MF * 16);
+    for (int o = tid; o < rows * NF * 16; o += WAVES * kWave) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) v += sums[w][o];
+        if (a.splits > 1)
+            mine[o] = v;
+        else
+            put1(a, o / (NF * 16), j0 + o % (NF * 16), v);
+    }
+    if (a.splits == 1 || !last_split(a.counters + strip, a.splits, &shared)) return;
+    const float *parts = a.parts + (int64_t)strip * a.splits * OUT;
+    for (int o = tid; o < rows * NF * 16; o += WAVES * kWave) {
+        float v = 0.0f;
+        for (int k = 0; k < a.splits; ++k) v += parts[(int64_t)k * OUT + o];  // in this order
+        put1(a, o / (NF * 16), j0 + o % (NF * 16), v);
+    }
+}
+
 // Tiles of out and splits of c for a kernel of bi x bj tiles whose steps take `depth` c's
 // and whose splits are whole turns of `turn` steps.
 void plan(MxProductArgs *a, int bi, int bj, int depth, int turn, void *workspace,
@@ -975,6 +1220,37 @@ hipError_t run_rows(MxProductArgs a, void *workspace, const MxDevice &dev, hipSt
 // `rows` of them within a 32-bit offset.
 bool dma_takes(const MxProductArgs &a, int64_t rows) {
     return (uintptr_t)a.p % 16 == 0 && a.ldp % 8 == 0 && a.ldp * 2 * rows < kReach;
+}
+
+// Rows of x up to which the kernel of few rows is taken.
+constexpr int kFewRows = 64;
+
+template <int LEFT, bool F8, int MF, int NF, int WAVES>
+hipError_t run_few(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
+    const int64_t strips = (a.J + NF * 16 - 1) / (NF * 16);
+    const int turns = (int)((a.q.nb + kTurn - 1) / kTurn);
+    int64_t splits = 1;
+    // strips that leave compute units idle are split, two turns of each wave at least
+    if (workspace && strips <= kMxCounters && strips < dev.cus) {
+        splits = dev.cus / strips;
+        splits = splits < turns / (2 * WAVES) ? splits : turns / (2 * WAVES);
+        splits = splits > 1 ? splits : 1;
+    }
+    a.split_steps = (int)((turns + splits - 1) / splits);
+    a.splits = a.split_steps > 0 ? (turns + a.split_steps - 1) / a.split_steps : 1;
+    a.counters = (uint32_t *)workspace;
+    a.parts = (float *)((char *)workspace + kMxCounterBytes);
+    mx_few<LEFT, F8, MF, NF, WAVES>
+        <<<dim3((uint32_t)(strips * a.splits)), dim3(WAVES * kWave), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <int LEFT, bool F8>
+hipError_t choose_few(const MxProductArgs &a, void *workspace, const MxDevice &dev,
+                      hipStream_t stream) {
+    if (a.I <= 16) return run_few<LEFT, F8, 1, 1, 8>(a, workspace, dev, stream);
+    if (a.I <= 32) return run_few<LEFT, F8, 2, 1, 8>(a, workspace, dev, stream);
+    return run_few<LEFT, F8, 4, 1, 8>(a, workspace, dev, stream);
 }
 
 template <bool F8>
@@ -1046,6 +1322,20 @@ hipError_t launch_mx_dequantize(int format, int dtype, const MxCastArgs &a, hipS
 hipError_t launch_mx_product(MxLeft left, int right, MxProductArgs a, void *workspace,
                              const MxDevice &dev, hipStream_t stream) {
     constexpr int c4 = kRightFp4 | kRightCols, c8 = kRightFp8 | kRightCols;
+    if (a.I <= kFewRows && right < kRightCols)
+        switch (left * 4 + right) {
+            case kLeftRows * 4 + kRightFp4:
+                return choose_few<kLeftRows, false>(a, workspace, dev, stream);
+            case kLeftRows * 4 + kRightFp8:
+                return choose_few<kLeftRows, true>(a, workspace, dev, stream);
+            case kLeftFp4 * 4 + kRightFp4:
+                return choose_few<kLeftFp4, false>(a, workspace, dev, stream);
+            case kLeftFp4 * 4 + kRightFp8:
+                return choose_few<kLeftFp4, true>(a, workspace, dev, stream);
+            case kLeftFp8 * 4 + kRightFp4:
+                return choose_few<kLeftFp8, false>(a, workspace, dev, stream);
+            default: return choose_few<kLeftFp8, true>(a, workspace, dev, stream);
+        }
     switch (left * 4 + right) {
         case kLeftRows * 4 + kRightFp4:
             if (a.q.nb >= 8 && dma_takes(a, 256))
