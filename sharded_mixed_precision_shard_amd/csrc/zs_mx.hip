@@ -429,22 +429,40 @@ __device__ __forceinline__ void put1(const MxProductArgs &a, int i, int j, float
         ((__bf16 *)a.out)[at] = (__bf16)v;
 }
 
-// Which of a tile's splits arrives last: it finds the others' sums in memory.
-// All threads call it after they have written theirs.
+// Sums on their way to the split that joins them.  The workgroups sit on XCDs whose L2
+// caches do not see each other's writes, so they are written and read by agent-scope
+// atomics, which go past those caches; a workgroup arrives when its own have been
+// acknowledged.
+__device__ __forceinline__ void put_part(float *at, f32x4 v) {
+    const uint64_t *w = (const uint64_t *)&v;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        __hip_atomic_store((uint64_t *)at + e, w[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4 get_part(const float *at) {
+    uint64_t w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        w[e] = __hip_atomic_load((const uint64_t *)at + e, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+    return f32x4{__uint_as_float((uint32_t)w[0]), __uint_as_float((uint32_t)(w[0] >> 32)),
+                 __uint_as_float((uint32_t)w[1]), __uint_as_float((uint32_t)(w[1] >> 32))};
+}
+
+// Whether this of a tile's splits arrives last: the others' sums are then in memory.  All
+// threads call it after they have put theirs; the counter is left at 0.
 __device__ __forceinline__ bool last_split(uint32_t *counter, int splits, uint32_t *shared) {
-    __threadfence();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
         const uint32_t before =
-            __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         const bool last = before == (uint32_t)splits - 1u;
         if (last) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         *shared = last;
     }
     __syncthreads();
-    const bool last = *shared != 0;
-    if (last) __threadfence();
-    return last;
+    return *shared != 0;
 }
 
 // Which tile a workgroup makes.  Workgroups are dealt to the XCDs in turn: each XCD
@@ -467,39 +485,41 @@ __device__ __forceinline__ void tile_of(int64_t block, int tiles_i, int tiles_j,
 // adds them.
 template <int BI, int BJ, int WI, int WJ>
 __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
-                                            const f32x16 (&acc)[BJ / WJ / 32][BI / WI / 32],
+                                            f32x16 (&acc)[BJ / WJ / 32][BI / WI / 32],
                                             int tile, int split, int i0, int j0, int wi, int wj,
                                             int wave, int lane, uint32_t *shared) {
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     // lane: i = lane % 32, and for each r four j's from 8 r + 4 (lane / 32)
     const int li = wi + lane % 32, lj = wj + lane / 32 * 4;
     if (a.splits > 1) {
-        float *mine = a.parts + ((int64_t)tile * a.splits + split) * (BI * BJ);
+        float *parts = a.parts + (int64_t)tile * a.splits * (BI * BJ) +
+                       wave * (FJ * FI * 1024) + lane * 4;
 #pragma unroll
         for (int j = 0; j < FJ; ++j)
 #pragma unroll
             for (int i = 0; i < FI; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    *(f32x4 *)(mine + (((wave * FJ + j) * FI + i) * 4 + r) * 256 + lane * 4) =
-                        f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
-                              acc[j][i][4 * r + 3]};
+                    put_part(parts + (int64_t)split * (BI * BJ) + ((j * FI + i) * 4 + r) * 256,
+                             f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
+                                   acc[j][i][4 * r + 3]});
         if (!last_split(a.counters + tile, a.splits, shared)) return;
-        const float *parts = a.parts + (int64_t)tile * a.splits * (BI * BJ);
 #pragma unroll
         for (int j = 0; j < FJ; ++j)
 #pragma unroll
-            for (int i = 0; i < FI; ++i)
+            for (int i = 0; i < FI; ++i) acc[j][i] = f32x16{};
+        for (int k = 0; k < a.splits; ++k)  // always in this order
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float *at =
-                        parts + (((wave * FJ + j) * FI + i) * 4 + r) * 256 + lane * 4;
-                    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-                    for (int k = 0; k < a.splits; ++k)  // always in this order
-                        v += *(const f32x4 *)(at + (int64_t)k * (BI * BJ));
-                    put4(a, i0 + li + 32 * i, j0 + lj + 32 * j + 8 * r, v);
-                }
-        return;
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int i = 0; i < FI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const f32x4 v = get_part(parts + (int64_t)k * (BI * BJ) +
+                                                 ((j * FI + i) * 4 + r) * 256);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][i][4 * r + e] += v[e];
+                    }
     }
 #pragma unroll
     for (int j = 0; j < FJ; ++j)
@@ -1156,7 +1176,7 @@ __global__ __launch_bounds__(WAVES *kWave) void mx_few(MxProductArgs a) {
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) v += sums[w][o];
         if (a.splits > 1)
-            mine[o] = v;
+            __hip_atomic_store(mine + o, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         else
             put1(a, o / (NF * 16), j0 + o % (NF * 16), v);
     }
@@ -1164,7 +1184,9 @@ __global__ __launch_bounds__(WAVES *kWave) void mx_few(MxProductArgs a) {
     const float *parts = a.parts + (int64_t)strip * a.splits * OUT;
     for (int o = tid; o < rows * NF * 16; o += WAVES * kWave) {
         float v = 0.0f;
-        for (int k = 0; k < a.splits; ++k) v += parts[(int64_t)k * OUT + o];  // in this order
+        for (int k = 0; k < a.splits; ++k)  // always in this order
+            v += __hip_atomic_load(parts + (int64_t)k * OUT + o, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
         put1(a, o / (NF * 16), j0 + o % (NF * 16), v);
     }
 }
@@ -1178,8 +1200,10 @@ void plan(MxProductArgs *a, int bi, int bj, int depth, int turn, void *workspace
     const int64_t tiles = (int64_t)a->tiles_i * a->tiles_j;
     const int steps = (a->C + depth - 1) / depth;
     int64_t splits = 1;
-    if (workspace && tiles <= kMxCounters && tiles < dev.cus) {
-        splits = dev.cus / tiles;
+    // two workgroups per compute unit, of a turn and eight steps at least
+    const int64_t groups = bi * bj > 128 * 128 ? dev.cus : 2 * dev.cus;
+    if (workspace && tiles <= kMxCounters && tiles < groups) {
+        splits = groups / tiles;
         splits = splits < steps / 8 ? splits : steps / 8;
         const int64_t room = kMxPartBytes / (tiles * bi * bj * 4);
         splits = splits < room ? splits : room;
@@ -1259,7 +1283,8 @@ hipError_t choose_rows(const MxProductArgs &a, void *workspace, const MxDevice &
     const int64_t out = (int64_t)a.I * a.J;
     if (out >= (int64_t)dev.cus * 256 * 256)
         return run_rows<256, 256, 2, 4, F8>(a, workspace, dev, stream);
-    return run_rows<128, 128, 2, 2, F8>(a, workspace, dev, stream);
+    if (a.I > 64) return run_rows<128, 128, 2, 2, F8>(a, workspace, dev, stream);
+    return run_rows<64, 128, 1, 4, F8>(a, workspace, dev, stream);
 }
 
 hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &dev,
@@ -1267,9 +1292,8 @@ hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &d
     const int64_t out = (int64_t)a.I * a.J;
     if (out >= (int64_t)dev.cus * 256 * 256)
         return run_fp4<256, 256, 2, 4>(a, workspace, dev, stream);
-    if (out >= (int64_t)dev.cus * 128 * 128)
-        return run_fp4<128, 128, 2, 2>(a, workspace, dev, stream);
-    return run_fp4<64, 64, 2, 2>(a, workspace, dev, stream);
+    if (a.I > 64) return run_fp4<128, 128, 2, 2>(a, workspace, dev, stream);
+    return run_fp4<64, 128, 1, 4>(a, workspace, dev, stream);
 }
 
 template <int LEFT, int RIGHT>
