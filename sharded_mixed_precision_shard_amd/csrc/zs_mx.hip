@@ -954,6 +954,174 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_rows(MxProductArgs a
     finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, (uint32_t *)lds0);
 }
 
+// dx = dy w and dw = dy^T x: the stored operand's rows run along the output, so a fragment
+// needs it transposed.  A thread loads a block two steps ahead, widens it and puts it into
+// LDS column-major, where the transposing reads take it from; dy goes there by DMA.  Both
+// operands' addresses move with c, so a 32-bit offset never passes a step; rows past the
+// last read as zeros.
+template <int BI, int BJ, int WI, int WJ, bool PC, bool F8>
+__global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_cols(MxProductArgs a) {
+    constexpr int NT = WI * WJ * kWave;
+    constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
+    constexpr int EACH = BI * 8 / NT;
+    constexpr int W = F8 ? 2 : 1;
+    constexpr int ROW = BJ / kMxBlock;  // blocks of a tile's row
+    static_assert(ROW * kStep == NT, "a thread for each block of a step");
+    __shared__ __attribute__((aligned(128))) char p0[BI * 128];
+    __shared__ __attribute__((aligned(128))) char p1[BI * 128];
+    __shared__ __attribute__((aligned(128))) char q0[BJ * 128];
+    __shared__ __attribute__((aligned(128))) char q1[BJ * 128];
+
+    const int tid = threadIdx.x, lane = tid % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int split = blockIdx.x % a.splits;
+    int ti, tj;
+    tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
+    const int tile = tj * a.tiles_i + ti, i0 = ti * BI, j0 = tj * BJ;
+    const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+    const int first = split * a.split_steps;
+    const int steps = min((a.C + kStep - 1) / kStep - first, a.split_steps);
+
+    // dy: rows of c (PC) or of i
+    const uint32_t p_row = (uint32_t)a.ldp * 2u;
+    const int64_t p_at = PC ? (int64_t)i0 * 2 : (int64_t)i0 * p_row;
+    uint32_t p_off;
+    int chunk = 0;
+    if constexpr (PC) {
+        // a wave's transfer k: whole rows of the tile, the 64-byte chunks permuted by c
+        constexpr int LANES = BI / 8, ROWS = kWave / LANES;
+        static_assert(ROWS >= 1, "a transfer holds whole rows");
+        const int c = wave * ROWS + lane / LANES;
+        // the permutation of a row is the same for every k: rows are NT / LANES apart
+        const int byte = at_cols<BI>(c, lane % LANES * 16) - c * (BI * 2);
+        p_off = (uint32_t)c * p_row + (uint32_t)byte;
+    } else {
+        const int row = wave * 8 + lane / 8;
+        chunk = (lane % 8) ^ (row & 7);
+        p_off = (uint32_t)row * p_row + (uint32_t)chunk * 16u;
+    }
+    auto fetch = [&](char *lds, int step) {
+        const int c0 = (first + step) * kStep;
+        if constexpr (PC) {
+            const int left = min(max(a.C - c0, 0), kStep);
+            const auto buf =
+                buffer_of((const char *)a.p + (int64_t)min(c0, a.C) * p_row + p_at,
+                          left > 0 ? (uint32_t)(left - 1) * p_row + (uint32_t)(a.I - i0) * 2u : 0u);
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+                dma16(buf, lds + (k * NT + wave * kWave) * 16,
+                      p_off + (uint32_t)(k * (NT / (BI / 8))) * p_row);
+        } else {
+            const auto buf = buffer_of((const char *)a.p + p_at, (uint32_t)min(a.I - i0, BI) * p_row);
+            // whole chunks only: the rest of a row is a step of its own
+            const uint32_t off = c0 + chunk * 8 + 8 <= a.C ? p_off + (uint32_t)c0 * 2u : kNowhere;
+#pragma unroll
+            for (int k = 0; k < EACH; ++k)
+                dma16(buf, lds + (k * (NT / 8) + wave * 8) * 128,
+                      off + (uint32_t)(k * (NT / 8)) * p_row);
+        }
+    };
+
+    const uint32_t q_row = (uint32_t)a.q.nb;
+    const int qc = tid / ROW, qb = tid % ROW;  // the thread's block of a step
+    struct Block {
+        u32x4 v[W];
+        uint32_t scale;
+    };
+    auto fetch_block = [&](int c0) {
+        const int left = min(max(a.C - c0, 0), kStep);
+        const int64_t at = (int64_t)min(c0, a.C) * q_row;
+        const int jb = j0 / kMxBlock;
+        const auto codes = buffer_of(a.q.codes + (at + jb) * (16 * W),
+                                     left > 0 ? ((uint32_t)left * q_row - jb) * (16u * W) : 0u);
+        const auto scales =
+            buffer_of(a.q.scales + at + jb, left > 0 ? (uint32_t)left * q_row - jb : 0u);
+        const uint32_t off = (uint32_t)qc * q_row + (uint32_t)qb;
+        Block b;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+            b.v[w] = __builtin_amdgcn_raw_buffer_load_b128(codes, off * (16 * W) + 16 * w, 0, 0);
+        b.scale = __builtin_amdgcn_raw_buffer_load_b8(scales, off, 0, 0);
+        return b;
+    };
+    auto put_block = [&](char *lds, const Block &b) {
+        const float s = scale_of(b.scale);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            u32x4 v;
+            if constexpr (F8)
+                v = widen_fp8(b.v[w / 2][w % 2 * 2], b.v[w / 2][w % 2 * 2 + 1], s);
+            else
+                v = widen_fp4(b.v[0][w], s);
+            *(u32x4 *)(lds + at_cols<BJ>(qc, qb * 64 + w * 16)) = v;
+        }
+    };
+
+    f32x16 acc[FJ][FI];
+#pragma unroll
+    for (int j = 0; j < FJ; ++j)
+#pragma unroll
+        for (int i = 0; i < FI; ++i) acc[j][i] = f32x16{};
+    auto multiply = [&](const char *p, const char *q) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            bf16x8 pf[FI], qf[FJ];
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) qf[j] = frag_cols<BJ>(q, wj + 32 * j, s, lane);
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+                pf[i] = PC ? frag_cols<BI>(p, wi + 32 * i, s, lane)
+                           : frag_rows(p, wi + 32 * i, s, lane);
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int i = 0; i < FI; ++i)
+                    acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[j], pf[i], acc[j][i], 0,
+                                                                        0, 0);
+        }
+    };
+
+    const int whole = a.C & ~7;
+    if (!PC && whole < a.C && split == 0) {  // fewer than 8 c's past the last whole chunk
+        PlainStage<BI, NT, false> rest;
+        rest.load(a.p, a.ldp, i0, a.I, whole, a.C, tid);
+        rest.store(p0, tid);
+        put_block(q0, fetch_block(whole));
+        __syncthreads();
+        multiply(p0, q0);
+        __syncthreads();
+    }
+
+    // A stage is ready when its transfers have ended; the loads of a block, W + 1 of them, are
+    // issued after those, which the scheduling barriers keep so, and may go on.
+    Block b0, b1;
+    fetch(p0, 0);
+    b0 = fetch_block(first * kStep);
+    put_block(q0, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    b1 = fetch_block((first + 1) * kStep);
+    // two steps a turn: a split ends with a whole turn, or with c, past which all is 0
+#pragma unroll 1
+    for (int step = 0; step < steps; step += 2) {
+        stage_ready<W + 1>();
+        fetch(p1, step + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        b0 = fetch_block((first + step + 2) * kStep);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(p0, q0);
+        put_block(q1, b1);
+        stage_ready<W + 1>();
+        fetch(p0, step + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        b1 = fetch_block((first + step + 3) * kStep);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(p1, q1);
+        put_block(q0, b0);
+    }
+    stage_ready<0>();
+    finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, (uint32_t *)p0);
+}
+
 // ------------------------------------------------------- products of few rows
 
 // Up to 16 MF rows of x: bound by the bytes of w, which every wave takes 16 NF rows of,
@@ -1246,8 +1414,11 @@ bool dma_takes(const MxProductArgs &a, int64_t rows) {
     return (uintptr_t)a.p % 16 == 0 && a.ldp % 8 == 0 && a.ldp * 2 * rows < kReach;
 }
 
-// Rows of x up to which the kernel of few rows is taken.
-constexpr int kFewRows = 64;
+// Rows of x up to which the kernel of few rows is taken: where a tiled kernel takes the
+// operands, too, it is faster from there on (K = 8192, N = 28672, bf16 x: 8 rows 38 us here and 46
+// in tiles of 32, 16 rows 42 and 47, 32 rows 129 and 48; fp4 x: 16 rows 35 and 40, 32 rows 50
+// and 41).
+constexpr int kFewRows = 64, kFewTiled = 16;
 
 template <int LEFT, bool F8, int MF, int NF, int WAVES>
 hipError_t run_few(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
@@ -1269,9 +1440,21 @@ hipError_t run_few(MxProductArgs a, void *workspace, const MxDevice &dev, hipStr
     return hipGetLastError();
 }
 
+// Strips of 64 columns read x a quarter as often as strips of 16, and leave a quarter of the
+// workgroups: bf16 x, K = 8192, N = 28672, 16 rows 42 us against 72, one row 36 and 38; K = 4096,
+// N = 11008, 16 rows 11.2 and 16.4, one row 10.3 and 9.2; N = 4096, 10.9 and 6.8.  An x in blocks
+// is short: strips of 16 are as fast or faster everywhere.
 template <int LEFT, bool F8>
 hipError_t choose_few(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                       hipStream_t stream) {
+    const int64_t wide = (a.I > 4 ? 32 : 64) * dev.cus;
+    if constexpr (LEFT == kLeftRows) {
+        if (a.J >= wide && a.I <= 16)
+            return run_few<LEFT, F8, 1, 4, 4>(a, workspace, dev, stream);
+        if (a.J >= wide && a.I <= 32)
+            return run_few<LEFT, F8, 2, 2, 4>(a, workspace, dev, stream);
+        if (a.J >= wide) return run_few<LEFT, F8, 4, 2, 4>(a, workspace, dev, stream);
+    }
     if (a.I <= 16) return run_few<LEFT, F8, 1, 1, 8>(a, workspace, dev, stream);
     if (a.I <= 32) return run_few<LEFT, F8, 2, 1, 8>(a, workspace, dev, stream);
     return run_few<LEFT, F8, 4, 1, 8>(a, workspace, dev, stream);
@@ -1284,7 +1467,24 @@ hipError_t choose_rows(const MxProductArgs &a, void *workspace, const MxDevice &
     if (out >= (int64_t)dev.cus * 256 * 256)
         return run_rows<256, 256, 2, 4, F8>(a, workspace, dev, stream);
     if (a.I > 64) return run_rows<128, 128, 2, 2, F8>(a, workspace, dev, stream);
-    return run_rows<64, 128, 1, 4, F8>(a, workspace, dev, stream);
+    if (a.I > 32) return run_rows<64, 128, 1, 4, F8>(a, workspace, dev, stream);
+    return run_rows<32, 128, 1, 4, F8>(a, workspace, dev, stream);
+}
+
+template <int BI, int BJ, int WI, int WJ, bool PC, bool F8>
+hipError_t run_cols(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
+    plan(&a, BI, BJ, kStep, 2, workspace, dev);
+    mx_tile_cols<BI, BJ, WI, WJ, PC, F8><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <bool PC, bool F8>
+hipError_t choose_cols(const MxProductArgs &a, void *workspace, const MxDevice &dev,
+                       hipStream_t stream) {
+    const int64_t out = (int64_t)a.I * a.J;
+    if (out >= (int64_t)dev.cus * 256 * 256 / 2)
+        return run_cols<256, 256, 2, 4, PC, F8>(a, workspace, dev, stream);
+    return run_cols<128, 128, 2, 2, PC, F8>(a, workspace, dev, stream);
 }
 
 hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &dev,
@@ -1293,7 +1493,8 @@ hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &d
     if (out >= (int64_t)dev.cus * 256 * 256)
         return run_fp4<256, 256, 2, 4>(a, workspace, dev, stream);
     if (a.I > 64) return run_fp4<128, 128, 2, 2>(a, workspace, dev, stream);
-    return run_fp4<64, 128, 1, 4>(a, workspace, dev, stream);
+    if (a.I > 32) return run_fp4<64, 128, 1, 4>(a, workspace, dev, stream);
+    return run_fp4<32, 128, 1, 4>(a, workspace, dev, stream);
 }
 
 template <int LEFT, int RIGHT>
@@ -1346,7 +1547,14 @@ hipError_t launch_mx_dequantize(int format, int dtype, const MxCastArgs &a, hipS
 hipError_t launch_mx_product(MxLeft left, int right, MxProductArgs a, void *workspace,
                              const MxDevice &dev, hipStream_t stream) {
     constexpr int c4 = kRightFp4 | kRightCols, c8 = kRightFp8 | kRightCols;
-    if (a.I <= kFewRows && right < kRightCols)
+    // what the kernels on whole chunks take
+    const bool rows = left == kLeftRows && a.q.nb >= 8 && dma_takes(a, 256);
+    const bool fp4 = left == kLeftFp4 && right == kRightFp4 && a.q.nb >= kStep4Blocks &&
+                     a.q.nb * 16 * 256 < kReach;
+    // dy^T's chunks lie along i, where a last one that is not whole could reach past the matrix
+    const bool cols = right >= kRightCols && dma_takes(a, 256) &&
+                      (left == kLeftRows || a.I % 8 == 0) && a.q.nb * 32 * kStep < kReach;
+    if (right < kRightCols && a.I <= (rows || fp4 ? kFewTiled : kFewRows))
         switch (left * 4 + right) {
             case kLeftRows * 4 + kRightFp4:
                 return choose_few<kLeftRows, false>(a, workspace, dev, stream);
@@ -1362,21 +1570,25 @@ hipError_t launch_mx_product(MxLeft left, int right, MxProductArgs a, void *work
         }
     switch (left * 4 + right) {
         case kLeftRows * 4 + kRightFp4:
-            if (a.q.nb >= 8 && dma_takes(a, 256))
-                return choose_rows<false>(a, workspace, dev, stream);
+            if (rows) return choose_rows<false>(a, workspace, dev, stream);
             return choose_tile<kLeftRows, kRightFp4>(a, workspace, dev, stream);
         case kLeftRows * 4 + kRightFp8:
-            if (a.q.nb >= 8 && dma_takes(a, 256))
-                return choose_rows<true>(a, workspace, dev, stream);
+            if (rows) return choose_rows<true>(a, workspace, dev, stream);
             return choose_tile<kLeftRows, kRightFp8>(a, workspace, dev, stream);
-        case kLeftRows * 4 + c4: return choose_tile<kLeftRows, c4>(a, workspace, dev, stream);
-        case kLeftRows * 4 + c8: return choose_tile<kLeftRows, c8>(a, workspace, dev, stream);
-        case kLeftCols * 4 + c4: return choose_tile<kLeftCols, c4>(a, workspace, dev, stream);
-        case kLeftCols * 4 + c8: return choose_tile<kLeftCols, c8>(a, workspace, dev, stream);
+        case kLeftRows * 4 + c4:
+            if (cols) return choose_cols<false, false>(a, workspace, dev, stream);
+            return choose_tile<kLeftRows, c4>(a, workspace, dev, stream);
+        case kLeftRows * 4 + c8:
+            if (cols) return choose_cols<false, true>(a, workspace, dev, stream);
+            return choose_tile<kLeftRows, c8>(a, workspace, dev, stream);
+        case kLeftCols * 4 + c4:
+            if (cols) return choose_cols<true, false>(a, workspace, dev, stream);
+            return choose_tile<kLeftCols, c4>(a, workspace, dev, stream);
+        case kLeftCols * 4 + c8:
+            if (cols) return choose_cols<true, true>(a, workspace, dev, stream);
+            return choose_tile<kLeftCols, c8>(a, workspace, dev, stream);
         case kLeftFp4 * 4 + kRightFp4:
-            // offsets inside a tile's rows are 32-bit numbers below kNowhere
-            if (a.q.nb >= kStep4Blocks && a.q.nb * 16 * 256 < (int64_t)kNowhere)
-                return choose_fp4(a, workspace, dev, stream);
+            if (fp4) return choose_fp4(a, workspace, dev, stream);
             return choose_tile<kLeftFp4, kRightFp4>(a, workspace, dev, stream);
         case kLeftFp4 * 4 + kRightFp8:
             return choose_tile<kLeftFp4, kRightFp8>(a, workspace, dev, stream);
