@@ -449,6 +449,17 @@ __device__ __forceinline__ f32x4 get_part(const float *at) {
                  __uint_as_float((uint32_t)w[1]), __uint_as_float((uint32_t)(w[1] >> 32))};
 }
 
+// Whether another workgroup has arrived at a counter, for all threads.
+__device__ __forceinline__ bool arrived(uint32_t *counter, uint32_t *shared) {
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *shared = __hip_atomic_load(counter, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    const bool yes = *shared != 0;
+    __syncthreads();
+    return yes;
+}
+
 // Whether this of a tile's splits arrives last: the others' sums are then in memory.  All
 // threads call it after they have put theirs; the counter is left at 0.
 __device__ __forceinline__ bool last_split(uint32_t *counter, int splits, uint32_t *shared) {
@@ -491,35 +502,43 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     // lane: i = lane % 32, and for each r four j's from 8 r + 4 (lane / 32)
     const int li = wi + lane % 32, lj = wj + lane / 32 * 4;
-    if (a.splits > 1) {
-        float *parts = a.parts + (int64_t)tile * a.splits * (BI * BJ) +
-                       wave * (FJ * FI * 1024) + lane * 4;
-#pragma unroll
-        for (int j = 0; j < FJ; ++j)
-#pragma unroll
-            for (int i = 0; i < FI; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    put_part(parts + (int64_t)split * (BI * BJ) + ((j * FI + i) * 4 + r) * 256,
-                             f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
-                                   acc[j][i][4 * r + 3]});
-        if (!last_split(a.counters + tile, a.splits, shared)) return;
-#pragma unroll
-        for (int j = 0; j < FJ; ++j)
-#pragma unroll
-            for (int i = 0; i < FI; ++i) acc[j][i] = f32x16{};
-        for (int k = 0; k < a.splits; ++k)  // always in this order
+    // Splits are joined two by two: of splits [s, s + n) and [s + n, s + 2 n) the one that is
+    // done first leaves its sums and ends, the other adds them to its own and goes on with
+    // both.  The tree is the same every time and an addition's two sides may change places,
+    // so the order in which splits end does not show.
+    float *parts = a.parts + (int64_t)tile * a.splits * (BI * BJ) + wave * (FJ * FI * 1024) +
+                   lane * 4;
+    for (int n = 1; n < a.splits; n *= 2) {
+        const int s = split & ~(2 * n - 1), other = split & n ? s : s + n;
+        if (other >= a.splits) continue;
+        uint32_t *counter = a.counters + (int64_t)tile * a.splits + s + n;
+        if (!arrived(counter, shared)) {
+            float *mine = parts + (int64_t)(split & ~(n - 1)) * (BI * BJ);
 #pragma unroll
             for (int j = 0; j < FJ; ++j)
 #pragma unroll
                 for (int i = 0; i < FI; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const f32x4 v = get_part(parts + (int64_t)k * (BI * BJ) +
-                                                 ((j * FI + i) * 4 + r) * 256);
+                    for (int r = 0; r < 4; ++r)
+                        put_part(mine + ((j * FI + i) * 4 + r) * 256,
+                                 f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1],
+                                       acc[j][i][4 * r + 2], acc[j][i][4 * r + 3]});
+            if (!last_split(counter, 2, shared)) return;
+        } else if (threadIdx.x == 0) {
+            __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        const float *theirs = parts + (int64_t)other * (BI * BJ);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[j][i][4 * r + e] += v[e];
-                    }
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const f32x4 v = get_part(theirs + ((j * FI + i) * 4 + r) * 256);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][i][4 * r + e] += v[e];
+                }
+        __syncthreads();  // `shared` is free again
     }
 #pragma unroll
     for (int j = 0; j < FJ; ++j)
@@ -1370,7 +1389,7 @@ void plan(MxProductArgs *a, int bi, int bj, int depth, int turn, void *workspace
     int64_t splits = 1;
     // two workgroups per compute unit, of a turn and eight steps at least
     const int64_t groups = bi * bj > 128 * 128 ? dev.cus : 2 * dev.cus;
-    if (workspace && tiles <= kMxCounters && tiles < groups) {
+    if (workspace && tiles < groups && groups <= kMxCounters) {
         splits = groups / tiles;
         splits = splits < steps / 8 ? splits : steps / 8;
         const int64_t room = kMxPartBytes / (tiles * bi * bj * 4);
