@@ -429,24 +429,26 @@ __device__ __forceinline__ void put1(const MxProductArgs &a, int i, int j, float
         ((__bf16 *)a.out)[at] = (__bf16)v;
 }
 
-// Sums on their way to the split that joins them.  The workgroups sit on XCDs whose L2
-// caches do not see each other's writes, so they are written and read by agent-scope
-// atomics, which go past those caches; a workgroup arrives when its own have been
-// acknowledged.
-__device__ __forceinline__ void put_part(float *at, f32x4 v) {
-    const uint64_t *w = (const uint64_t *)&v;
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        __hip_atomic_store((uint64_t *)at + e, w[e], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Memory of fewer than 2^31 bytes that instructions address by 32-bit offsets: reads past
+// its end give zeros.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
 }
-__device__ __forceinline__ f32x4 get_part(const float *at) {
-    uint64_t w[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-        w[e] = __hip_atomic_load((const uint64_t *)at + e, __ATOMIC_RELAXED,
-                                 __HIP_MEMORY_SCOPE_AGENT);
-    return f32x4{__uint_as_float((uint32_t)w[0]), __uint_as_float((uint32_t)(w[0] >> 32)),
-                 __uint_as_float((uint32_t)w[1]), __uint_as_float((uint32_t)(w[1] >> 32))};
+
+// Sums on their way to the split that joins them.  The workgroups sit on XCDs whose L2
+// caches do not see each other's writes, so they are written and read past those caches
+// (sc1, as agent-scope atomics are, but 16 bytes at a time); a workgroup arrives when its own
+// have been acknowledged.
+constexpr int kPastL2 = 16;
+__device__ __forceinline__ void put_part(float *parts, uint32_t at, f32x4 v) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v),
+                                           buffer_of(parts, (uint32_t)kMxPartBytes), at * 4u, 0,
+                                           kPastL2);
+}
+__device__ __forceinline__ f32x4 get_part(const float *parts, uint32_t at) {
+    return __builtin_bit_cast(
+        f32x4, __builtin_amdgcn_raw_buffer_load_b128(buffer_of(parts, (uint32_t)kMxPartBytes),
+                                                     at * 4u, 0, kPastL2));
 }
 
 // Whether another workgroup has arrived at a counter, for all threads.
@@ -492,6 +494,49 @@ __device__ __forceinline__ void tile_of(int64_t block, int tiles_i, int tiles_j,
     *j = (int)(in / rows);
 }
 
+// The wave groups of a workgroup, each with a part of c: all but the first leave their sums
+// in LDS, a tile of them each in a and b (what fits a, and the rest in b), and the first
+// adds them in order.  True for the first.
+template <int KG, int FJ, int FI>
+__device__ __forceinline__ bool join_groups(f32x16 (&acc)[FJ][FI], char *a, char *b, int a_bytes,
+                                            int tile_bytes, int group, int wave, int lane) {
+    if constexpr (KG == 1) return true;
+    const int in_a = a_bytes / tile_bytes;
+    auto at = [&](int g) {
+        char *p = g - 1 < in_a ? a + (g - 1) * tile_bytes : b + (g - 1 - in_a) * tile_bytes;
+        return (f32x4 *)(p + wave * (FJ * FI * 4096)) + lane;
+    };
+    if (group > 0) {
+        f32x4 *to = at(group);
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    to[((j * FI + i) * 4 + r) * kWave] =
+                        f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
+                              acc[j][i][4 * r + 3]};
+    }
+    __syncthreads();
+    if (group > 0) return false;
+#pragma unroll
+    for (int g = 1; g < KG; ++g) {
+        const f32x4 *from = at(g);
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const f32x4 v = from[((j * FI + i) * 4 + r) * kWave];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[j][i][4 * r + e] += v[e];
+                }
+    }
+    return true;
+}
+
 // The end of a tile: its sums go out, or to the workspace, where the last of the splits
 // adds them.
 template <int BI, int BJ, int WI, int WJ>
@@ -506,35 +551,35 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
     // done first leaves its sums and ends, the other adds them to its own and goes on with
     // both.  The tree is the same every time and an addition's two sides may change places,
     // so the order in which splits end does not show.
-    float *parts = a.parts + (int64_t)tile * a.splits * (BI * BJ) + wave * (FJ * FI * 1024) +
-                   lane * 4;
+    const uint32_t here = (uint32_t)wave * (FJ * FI * 1024) + (uint32_t)lane * 4;
+    const uint32_t slots = (uint32_t)tile * (uint32_t)a.splits;
     for (int n = 1; n < a.splits; n *= 2) {
         const int s = split & ~(2 * n - 1), other = split & n ? s : s + n;
         if (other >= a.splits) continue;
         uint32_t *counter = a.counters + (int64_t)tile * a.splits + s + n;
         if (!arrived(counter, shared)) {
-            float *mine = parts + (int64_t)(split & ~(n - 1)) * (BI * BJ);
+            const uint32_t mine = (slots + (uint32_t)(split & ~(n - 1))) * (BI * BJ) + here;
 #pragma unroll
             for (int j = 0; j < FJ; ++j)
 #pragma unroll
                 for (int i = 0; i < FI; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        put_part(mine + ((j * FI + i) * 4 + r) * 256,
+                        put_part(a.parts, mine + ((j * FI + i) * 4 + r) * 256,
                                  f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1],
                                        acc[j][i][4 * r + 2], acc[j][i][4 * r + 3]});
             if (!last_split(counter, 2, shared)) return;
         } else if (threadIdx.x == 0) {
             __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        const float *theirs = parts + (int64_t)other * (BI * BJ);
+        const uint32_t theirs = (slots + (uint32_t)other) * (BI * BJ) + here;
 #pragma unroll
         for (int j = 0; j < FJ; ++j)
 #pragma unroll
             for (int i = 0; i < FI; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const f32x4 v = get_part(theirs + ((j * FI + i) * 4 + r) * 256);
+                    const f32x4 v = get_part(a.parts, theirs + ((j * FI + i) * 4 + r) * 256);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[j][i][4 * r + e] += v[e];
                 }
@@ -551,26 +596,34 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
                            acc[j][i][4 * r + 3]});
 }
 
-// A workgroup makes a BI x BJ tile of out (of one split of c).  The matrix
+// The steps that each wave group of a split takes; past the last c all reads as 0.
+template <int KG>
+__device__ __forceinline__ int group_steps(const MxProductArgs &a, int depth, int split) {
+    return min((a.C + depth - 1) / depth - split * KG * a.split_steps, a.split_steps);
+}
+
+// A workgroup makes a BI x BJ tile of out (of one split of c, in KG wave groups).  The matrix
 // instruction takes Q's rows as its rows and P's as its columns: a lane then
 // holds four neighbouring j's of one i, and stores them together.
-template <int BI, int BJ, int WI, int WJ, int LEFT, int RIGHT>
-__global__ __launch_bounds__(WI *WJ *kWave) void mx_tile(MxProductArgs a) {
+template <int BI, int BJ, int WI, int WJ, int KG, int LEFT, int RIGHT>
+__global__ __launch_bounds__(WI *WJ *KG *kWave) void mx_tile(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     constexpr bool PC = LEFT == kLeftCols, QC = (RIGHT & kRightCols) != 0;
     constexpr bool P_HELD = LEFT == kLeftFp4 || LEFT == kLeftFp8;
     constexpr int P_BYTES = BI * kStep * 2, Q_BYTES = BJ * kStep * 2;
-    __shared__ __attribute__((aligned(128))) char lds[2 * (P_BYTES + Q_BYTES)];
+    __shared__ __attribute__((aligned(128))) char all[KG][2 * (P_BYTES + Q_BYTES)];
 
-    const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    const int tid = threadIdx.x % NT, lane = tid % kWave, wave = tid / kWave;
+    char *lds = all[group];
     const int split = blockIdx.x % a.splits;
     int ti, tj;
     tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
     const int tile = tj * a.tiles_i + ti, i0 = ti * BI, j0 = tj * BJ;
     const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
-    const int first = split * a.split_steps;
-    const int steps = min((a.C + kStep - 1) / kStep - first, a.split_steps);
+    const int first = (split * KG + group) * a.split_steps;
+    const int steps = group_steps<KG>(a, kStep, split);
 
     f32x16 acc[FJ][FI];
 #pragma unroll
@@ -624,7 +677,10 @@ __global__ __launch_bounds__(WI *WJ *kWave) void mx_tile(MxProductArgs a) {
         if (more) store((step + 1) % 2);
     }
 
-    finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, (uint32_t *)lds);
+    if (KG > 1) __syncthreads();
+    if (join_groups<KG>(acc, all[0], all[0], (int)sizeof(all), BI * BJ * 4, group, wave, lane))
+        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
+                                    (uint32_t *)all);
 }
 
 // ---------------------------------------------- products of two fp4 operands
@@ -638,12 +694,9 @@ constexpr int kStep4Blocks = kStep4 / kMxBlock;
 typedef __attribute__((address_space(3))) void lds_void;
 struct __attribute__((packed, aligned(1))) Bytes8 { uint64_t v; };
 
-// From memory to LDS past the registers: lane l's 16 bytes go to lds + 16 l.  Reads
-// past the buffer's size give zeros; kNowhere, and what is added to it, is past every size.
+// From memory to LDS past the registers: lane l's 16 bytes go to lds + 16 l.  kNowhere, and
+// what is added to it, is past every buffer's size.
 constexpr uint32_t kNowhere = 0x80000000u;
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void *p, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
-}
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t from, char *lds, uint32_t offset) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (lds_void *)lds, 16, (int)offset, 0, 0, 0);
 }
@@ -673,21 +726,24 @@ struct Scales8 {
 // Both operands' codes go into the scaled matrix instruction as they are: 64 products
 // of a row and a column per instruction, at four times the rate of bf16.  A lane holds
 // a block of 32, so its scale is one byte, taken from a word of four by number.
-template <int BI, int BJ, int WI, int WJ>
-__global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_fp4(MxProductArgs a) {
+template <int BI, int BJ, int WI, int WJ, int KG>
+__global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     constexpr int P_BYTES = BI * 128, Q_BYTES = BJ * 128;
     constexpr int EACH_P = BI * 8 / NT, EACH_Q = BJ * 8 / NT;
     // two stages, each an array of its own: the compiler sees that what is read of one
     // does not wait for what is on its way into the other
-    __shared__ __attribute__((aligned(128))) char lds0[P_BYTES + Q_BYTES];
-    __shared__ __attribute__((aligned(128))) char lds1[P_BYTES + Q_BYTES];
-    __shared__ uint64_t scales0[NT];
-    __shared__ uint64_t scales1[NT];
+    __shared__ __attribute__((aligned(128))) char all0[KG][P_BYTES + Q_BYTES];
+    __shared__ __attribute__((aligned(128))) char all1[KG][P_BYTES + Q_BYTES];
+    __shared__ uint64_t all_scales0[KG][NT];
+    __shared__ uint64_t all_scales1[KG][NT];
 
-    const int tid = threadIdx.x, lane = tid % kWave;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    const int tid = threadIdx.x % NT, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    char *lds0 = all0[group], *lds1 = all1[group];
+    uint64_t *scales0 = all_scales0[group], *scales1 = all_scales1[group];
     const int split = blockIdx.x % a.splits;
     int ti, tj;
     tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
@@ -695,8 +751,8 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_fp4(MxProductArgs a)
     const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
     const int nb = (int)a.q.nb;
     const uint32_t row_bytes = (uint32_t)nb * 16u;
-    const int first = split * a.split_steps;
-    const int steps = min((nb + kStep4Blocks - 1) / kStep4Blocks - first, a.split_steps);
+    const int first = (split * KG + group) * a.split_steps;
+    const int steps = group_steps<KG>(a, kStep4, split);
 
     const auto p_buf = buffer_of(a.px.codes + (int64_t)i0 * row_bytes,
                                  (uint32_t)min(a.I - i0, BI) * row_bytes);
@@ -786,8 +842,10 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_fp4(MxProductArgs a)
         multiply(lds1, scales1);
         scales0[tid] = s.value();
     }
-    finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
-                                (uint32_t *)scales1);
+    if (KG > 1) stage_ready<0>();
+    if (join_groups<KG>(acc, all0[0], all1[0], (int)sizeof(all0), BI * BJ * 4, group, wave, lane))
+        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
+                                    (uint32_t *)all_scales0);
 }
 
 // ------------------------------------- bf16 against blocks, rows in full chunks
@@ -800,27 +858,29 @@ constexpr int64_t kReach = int64_t(1) << 31;
 // loads the block that it multiplies straight into registers, three steps ahead, and
 // widens it there, so LDS carries only x.  Half a wave (32 rows of w) takes one of a
 // step's two blocks, and the four instructions of a step its four words.
-template <int BI, int BJ, int WI, int WJ, bool F8>
-__global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_rows(MxProductArgs a) {
+template <int BI, int BJ, int WI, int WJ, int KG, bool F8>
+__global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     constexpr int EACH = BI * 8 / NT;
     constexpr int W = F8 ? 2 : 1;
-    __shared__ __attribute__((aligned(128))) char lds0[BI * 128];
-    __shared__ __attribute__((aligned(128))) char lds1[BI * 128];
-    __shared__ __attribute__((aligned(128))) char lds2[BI * 128];
-    __shared__ __attribute__((aligned(128))) char lds3[BI * 128];
+    __shared__ __attribute__((aligned(128))) char all0[KG][BI * 128];
+    __shared__ __attribute__((aligned(128))) char all1[KG][BI * 128];
+    __shared__ __attribute__((aligned(128))) char all2[KG][BI * 128];
+    __shared__ __attribute__((aligned(128))) char all3[KG][BI * 128];
 
-    const int tid = threadIdx.x, lane = tid % kWave;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    const int tid = threadIdx.x % NT, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    char *lds0 = all0[group], *lds1 = all1[group], *lds2 = all2[group], *lds3 = all3[group];
     const int split = blockIdx.x % a.splits;
     int ti, tj;
     tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
     const int tile = tj * a.tiles_i + ti, i0 = ti * BI, j0 = tj * BJ;
     const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
     const int nb = (int)a.q.nb;
-    const int first = split * a.split_steps;
-    const int steps = min((a.C + kStep - 1) / kStep - first, a.split_steps);
+    const int first = (split * KG + group) * a.split_steps;
+    const int steps = group_steps<KG>(a, kStep, split);
     const int r = lane % 32, h = lane / 32;
 
     const uint32_t row_bytes = (uint32_t)a.ldp * 2u;
@@ -890,7 +950,7 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_rows(MxProductArgs a
     };
     // what a row holds past its last whole chunk, fewer than 8 elements
     const int whole = a.C & ~7;
-    if (whole < a.C && split == 0) {
+    if (whole < a.C && split == 0 && group == 0) {
         const int at = whole % kMxBlock / 8;
 #pragma unroll
         for (int j = 0; j < FJ; ++j) {
@@ -970,7 +1030,9 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_rows(MxProductArgs a
     }
 #undef ZS_MX_STEP
     stage_ready<0>();
-    finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, (uint32_t *)lds0);
+    if (join_groups<KG>(acc, all0[0], all1[0], (int)sizeof(all0), BI * BJ * 4, group, wave, lane))
+        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
+                                    (uint32_t *)all3);
 }
 
 // dx = dy w and dw = dy^T x: the stored operand's rows run along the output, so a fragment
@@ -978,28 +1040,30 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_rows(MxProductArgs a
 // LDS column-major, where the transposing reads take it from; dy goes there by DMA.  Both
 // operands' addresses move with c, so a 32-bit offset never passes a step; rows past the
 // last read as zeros.
-template <int BI, int BJ, int WI, int WJ, bool PC, bool F8>
-__global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_cols(MxProductArgs a) {
+template <int BI, int BJ, int WI, int WJ, int KG, bool PC, bool F8>
+__global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     constexpr int EACH = BI * 8 / NT;
     constexpr int W = F8 ? 2 : 1;
     constexpr int ROW = BJ / kMxBlock;  // blocks of a tile's row
-    static_assert(ROW * kStep == NT, "a thread for each block of a step");
-    __shared__ __attribute__((aligned(128))) char p0[BI * 128];
-    __shared__ __attribute__((aligned(128))) char p1[BI * 128];
-    __shared__ __attribute__((aligned(128))) char q0[BJ * 128];
-    __shared__ __attribute__((aligned(128))) char q1[BJ * 128];
+    static_assert(ROW * kStep <= NT, "a thread for each block of a step");
+    __shared__ __attribute__((aligned(128))) char all_p0[KG][BI * 128];
+    __shared__ __attribute__((aligned(128))) char all_p1[KG][BI * 128];
+    __shared__ __attribute__((aligned(128))) char all_q0[KG][BJ * 128];
+    __shared__ __attribute__((aligned(128))) char all_q1[KG][BJ * 128];
 
-    const int tid = threadIdx.x, lane = tid % kWave;
+    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
+    const int tid = threadIdx.x % NT, lane = tid % kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    char *p0 = all_p0[group], *p1 = all_p1[group], *q0 = all_q0[group], *q1 = all_q1[group];
     const int split = blockIdx.x % a.splits;
     int ti, tj;
     tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
     const int tile = tj * a.tiles_i + ti, i0 = ti * BI, j0 = tj * BJ;
     const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
-    const int first = split * a.split_steps;
-    const int steps = min((a.C + kStep - 1) / kStep - first, a.split_steps);
+    const int first = (split * KG + group) * a.split_steps;
+    const int steps = group_steps<KG>(a, kStep, split);
 
     // dy: rows of c (PC) or of i
     const uint32_t p_row = (uint32_t)a.ldp * 2u;
@@ -1064,6 +1128,7 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_cols(MxProductArgs a
         return b;
     };
     auto put_block = [&](char *lds, const Block &b) {
+        if (ROW * kStep < NT && qc >= kStep) return;
         const float s = scale_of(b.scale);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
@@ -1102,10 +1167,11 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_cols(MxProductArgs a
 
     const int whole = a.C & ~7;
     if (!PC && whole < a.C && split == 0) {  // fewer than 8 c's past the last whole chunk
+        const int c0 = group == 0 ? whole : a.C;  // the other groups add zeros
         PlainStage<BI, NT, false> rest;
-        rest.load(a.p, a.ldp, i0, a.I, whole, a.C, tid);
+        rest.load(a.p, a.ldp, i0, a.I, c0, a.C, tid);
         rest.store(p0, tid);
-        put_block(q0, fetch_block(whole));
+        put_block(q0, fetch_block(c0));
         __syncthreads();
         multiply(p0, q0);
         __syncthreads();
@@ -1138,7 +1204,10 @@ __global__ __launch_bounds__(WI *WJ *kWave, 2) void mx_tile_cols(MxProductArgs a
         put_block(q0, b0);
     }
     stage_ready<0>();
-    finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, (uint32_t *)p0);
+    if (join_groups<KG>(acc, all_p0[0], all_p1[0], (int)sizeof(all_p0), BI * BJ * 4, group, wave,
+                        lane))
+        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
+                                    (uint32_t *)all_q0);
 }
 
 // ------------------------------------------------------- products of few rows
@@ -1379,51 +1448,59 @@ __global__ __launch_bounds__(WAVES *kWave) void mx_few(MxProductArgs a) {
 }
 
 // Tiles of out and splits of c for a kernel of bi x bj tiles whose steps take `depth` c's
-// and whose splits are whole turns of `turn` steps.
-void plan(MxProductArgs *a, int bi, int bj, int depth, int turn, void *workspace,
+// and whose splits are `groups` parts of whole turns of `turn` steps each.
+void plan(MxProductArgs *a, int bi, int bj, int groups, int depth, int turn, void *workspace,
           const MxDevice &dev) {
     a->tiles_i = (a->I + bi - 1) / bi;
     a->tiles_j = (a->J + bj - 1) / bj;
     const int64_t tiles = (int64_t)a->tiles_i * a->tiles_j;
     const int steps = (a->C + depth - 1) / depth;
     int64_t splits = 1;
-    // two workgroups per compute unit, of a turn and eight steps at least
-    const int64_t groups = bi * bj > 128 * 128 ? dev.cus : 2 * dev.cus;
-    if (workspace && tiles < groups && groups <= kMxCounters) {
-        splits = groups / tiles;
-        splits = splits < steps / 8 ? splits : steps / 8;
+    // a workgroup per compute unit, two where they are small
+    const int64_t most = groups == 1 && bi * bj <= 64 * 128 ? 2 * dev.cus : dev.cus;
+    if (workspace && tiles < most && most <= kMxCounters) {
+        splits = most / tiles;
+        splits = splits < steps / (8 * groups) ? splits : steps / (8 * groups);
         const int64_t room = kMxPartBytes / (tiles * bi * bj * 4);
         splits = splits < room ? splits : room;
         splits = splits > 1 ? splits : 1;
     }
-    a->split_steps = steps > 0 ? (int)((steps + splits - 1) / splits + turn - 1) / turn * turn : 0;
-    a->splits = steps > 0 ? (steps + a->split_steps - 1) / a->split_steps : 1;
+    const int64_t parts = splits * groups;
+    a->split_steps = steps > 0 ? (int)((steps + parts - 1) / parts + turn - 1) / turn * turn : 0;
+    const int64_t each = (int64_t)a->split_steps * groups;
+    a->splits = steps > 0 ? (int)((steps + each - 1) / each) : 1;
     a->counters = (uint32_t *)workspace;
     a->parts = (float *)((char *)workspace + kMxCounterBytes);
 }
+
+// Depth from which an output of few tiles is made in large ones all the same.
+constexpr int kLong = 8192;
 
 dim3 grid_of(const MxProductArgs &a) {
     return dim3((uint32_t)((int64_t)a.tiles_i * a.tiles_j * a.splits));
 }
 
-template <int BI, int BJ, int WI, int WJ, int LEFT, int RIGHT>
+template <int BI, int BJ, int WI, int WJ, int KG, int LEFT, int RIGHT>
 hipError_t run_tile(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    plan(&a, BI, BJ, kStep, 1, workspace, dev);
-    mx_tile<BI, BJ, WI, WJ, LEFT, RIGHT><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    plan(&a, BI, BJ, KG, kStep, 1, workspace, dev);
+    mx_tile<BI, BJ, WI, WJ, KG, LEFT, RIGHT>
+        <<<grid_of(a), dim3(WI * WJ * KG * kWave), 0, stream>>>(a);
     return hipGetLastError();
 }
 
-template <int BI, int BJ, int WI, int WJ>
+template <int BI, int BJ, int WI, int WJ, int KG>
 hipError_t run_fp4(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    plan(&a, BI, BJ, kStep4, 2, workspace, dev);
-    mx_tile_fp4<BI, BJ, WI, WJ><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    plan(&a, BI, BJ, KG, kStep4, 2, workspace, dev);
+    mx_tile_fp4<BI, BJ, WI, WJ, KG>
+        <<<grid_of(a), dim3(WI * WJ * KG * kWave), 0, stream>>>(a);
     return hipGetLastError();
 }
 
-template <int BI, int BJ, int WI, int WJ, bool F8>
+template <int BI, int BJ, int WI, int WJ, int KG, bool F8>
 hipError_t run_rows(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    plan(&a, BI, BJ, kStep, 4, workspace, dev);
-    mx_tile_rows<BI, BJ, WI, WJ, F8><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    plan(&a, BI, BJ, KG, kStep, 4, workspace, dev);
+    mx_tile_rows<BI, BJ, WI, WJ, KG, F8>
+        <<<grid_of(a), dim3(WI * WJ * KG * kWave), 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -1484,16 +1561,24 @@ hipError_t choose_rows(const MxProductArgs &a, void *workspace, const MxDevice &
                        hipStream_t stream) {
     const int64_t out = (int64_t)a.I * a.J;
     if (out >= (int64_t)dev.cus * 256 * 256)
-        return run_rows<256, 256, 2, 4, F8>(a, workspace, dev, stream);
-    if (a.I > 64) return run_rows<128, 128, 2, 2, F8>(a, workspace, dev, stream);
-    if (a.I > 32) return run_rows<64, 128, 1, 4, F8>(a, workspace, dev, stream);
-    return run_rows<32, 128, 1, 4, F8>(a, workspace, dev, stream);
+        return run_rows<256, 256, 2, 4, 1, F8>(a, workspace, dev, stream);
+    if (out >= (int64_t)dev.cus * 128 * 128)
+        return run_rows<128, 128, 2, 2, 1, F8>(a, workspace, dev, stream);
+    if (a.I <= 32 && a.J >= 64 * dev.cus)
+        return run_rows<32, 128, 1, 4, 1, F8>(a, workspace, dev, stream);
+    if (a.I <= 64 && a.J >= 64 * dev.cus)
+        return run_rows<64, 128, 1, 4, 1, F8>(a, workspace, dev, stream);
+    if (a.I <= 32) return run_rows<32, 128, 1, 4, 2, F8>(a, workspace, dev, stream);
+    if (a.I > 64 && a.C >= kLong)
+        return run_rows<128, 128, 2, 2, 2, F8>(a, workspace, dev, stream);
+    return run_rows<64, 64, 2, 2, 2, F8>(a, workspace, dev, stream);
 }
 
-template <int BI, int BJ, int WI, int WJ, bool PC, bool F8>
+template <int BI, int BJ, int WI, int WJ, int KG, bool PC, bool F8>
 hipError_t run_cols(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    plan(&a, BI, BJ, kStep, 2, workspace, dev);
-    mx_tile_cols<BI, BJ, WI, WJ, PC, F8><<<grid_of(a), dim3(WI * WJ * kWave), 0, stream>>>(a);
+    plan(&a, BI, BJ, KG, kStep, 2, workspace, dev);
+    mx_tile_cols<BI, BJ, WI, WJ, KG, PC, F8>
+        <<<grid_of(a), dim3(WI * WJ * KG * kWave), 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -1502,26 +1587,37 @@ hipError_t choose_cols(const MxProductArgs &a, void *workspace, const MxDevice &
                        hipStream_t stream) {
     const int64_t out = (int64_t)a.I * a.J;
     if (out >= (int64_t)dev.cus * 256 * 256 / 2)
-        return run_cols<256, 256, 2, 4, PC, F8>(a, workspace, dev, stream);
-    return run_cols<128, 128, 2, 2, PC, F8>(a, workspace, dev, stream);
+        return run_cols<256, 256, 2, 4, 1, PC, F8>(a, workspace, dev, stream);
+    if (out >= (int64_t)dev.cus * 128 * 128)
+        return run_cols<128, 128, 2, 2, 1, PC, F8>(a, workspace, dev, stream);
+    if (a.C >= kLong) return run_cols<128, 128, 2, 2, 2, PC, F8>(a, workspace, dev, stream);
+    return run_cols<64, 64, 2, 2, 4, PC, F8>(a, workspace, dev, stream);
 }
 
 hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                       hipStream_t stream) {
     const int64_t out = (int64_t)a.I * a.J;
     if (out >= (int64_t)dev.cus * 256 * 256)
-        return run_fp4<256, 256, 2, 4>(a, workspace, dev, stream);
-    if (a.I > 64) return run_fp4<128, 128, 2, 2>(a, workspace, dev, stream);
-    if (a.I > 32) return run_fp4<64, 128, 1, 4>(a, workspace, dev, stream);
-    return run_fp4<32, 128, 1, 4>(a, workspace, dev, stream);
+        return run_fp4<256, 256, 2, 4, 1>(a, workspace, dev, stream);
+    if (out >= (int64_t)dev.cus * 128 * 128)
+        return run_fp4<128, 128, 2, 2, 1>(a, workspace, dev, stream);
+    if (a.I <= 32 && a.J >= 64 * dev.cus)
+        return run_fp4<32, 128, 1, 4, 1>(a, workspace, dev, stream);
+    if (a.I <= 64 && a.J >= 64 * dev.cus)
+        return run_fp4<64, 128, 1, 4, 1>(a, workspace, dev, stream);
+    if (a.I > 64 && a.C >= kLong) return run_fp4<128, 128, 2, 2, 2>(a, workspace, dev, stream);
+    if (a.I > 32) return run_fp4<64, 64, 2, 2, 4>(a, workspace, dev, stream);
+    return run_fp4<32, 128, 1, 4, 2>(a, workspace, dev, stream);
 }
 
 template <int LEFT, int RIGHT>
 hipError_t choose_tile(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                        hipStream_t stream) {
     if ((int64_t)a.I * a.J >= (int64_t)dev.cus * 128 * 128)
-        return run_tile<128, 128, 2, 2, LEFT, RIGHT>(a, workspace, dev, stream);
-    return run_tile<64, 64, 2, 2, LEFT, RIGHT>(a, workspace, dev, stream);
+        return run_tile<128, 128, 2, 2, 1, LEFT, RIGHT>(a, workspace, dev, stream);
+    if (a.I > 64 && a.C >= kLong)
+        return run_tile<128, 128, 2, 2, 2, LEFT, RIGHT>(a, workspace, dev, stream);
+    return run_tile<64, 64, 2, 2, 4, LEFT, RIGHT>(a, workspace, dev, stream);
 }
 
 
