@@ -1212,6 +1212,20 @@ def mx_row_bytes(format: str, cols: int) -> int:
     return -(-int(cols) // ZS_MX_BLOCK) * (16 if format == "fp4" else 32)
 
 
+_BYTES = -1
+_MATRIX_TYPE = {**ZS_DTYPE, "torch.int16": 0, "torch.uint16": 0, "torch.uint8": _BYTES}
+
+
+@functools.lru_cache(maxsize=None)
+def _type_code(dtype):
+    return _MATRIX_TYPE.get(str(dtype))
+
+
+def _matrix_type(x):
+    """Element type of a matrix (ZS_DTYPE), _BYTES, or None for any other."""
+    return _type_code(x.dtype)
+
+
 class Mx:
     """A matrix held in blocks of 32 elements along its rows (see include/zs.h):
     ``codes`` and ``scales`` are uint8 tensors of mx_row_bytes(format, cols) and
@@ -1219,25 +1233,40 @@ class Mx:
     tensors are referenced for the object's lifetime.  :meth:`empty` makes them."""
 
     def __init__(self, codes, scales, cols, format):
-        if format not in ZS_MX_FORMAT:
+        code = ZS_MX_FORMAT.get(format)
+        if code is None:
             raise ValueError("format: expected 'fp4' or 'fp8', got %r" % (format,))
-        _check_type((codes,), ("torch.uint8",), "codes")
-        _check_type((scales,), ("torch.uint8",), "scales")
+        if _matrix_type(codes) != _BYTES or _matrix_type(scales) != _BYTES:
+            _check_type((codes,), ("torch.uint8",), "codes")
+            _check_type((scales,), ("torch.uint8",), "scales")
         cols = int(cols)
         if cols < 0:
             raise ValueError("cols must not be negative")
-        blocks, width = -(-cols // ZS_MX_BLOCK), mx_row_bytes(format, cols)
-        rows = scales.numel() // blocks if blocks else int(scales.shape[0])
-        if scales.numel() != rows * blocks or codes.numel() != rows * width:
+        blocks = (cols + 31) // 32
+        width = blocks * (16 if code == 0 else 32)
+        held = scales.numel()
+        rows = held // blocks if blocks else int(scales.shape[0])
+        if held != rows * blocks or codes.numel() != rows * width:
             raise ValueError("codes hold %d bytes and scales %d: no whole rows of %d and %d"
-                             % (codes.numel(), scales.numel(), width, blocks))
+                             % (codes.numel(), held, width, blocks))
         self.codes, self.scales, self.format = codes, scales, format
-        self.rows, self.cols, self.shape = rows, cols, (rows, cols)
-        self.device = codes.device
-        self.index = _same_device((codes, scales))
-        self.struct = ZsMx(_dev(codes, rows * width, "codes"),
-                           _dev(scales, rows * blocks, "scales"), rows, cols,
-                           ZS_MX_FORMAT[format], 0)
+        self.rows, self.cols = rows, cols
+        self.index = codes.get_device()
+        if scales.get_device() != self.index:
+            raise ValueError("codes and scales are on different devices")
+        if not (self.index >= 0 and codes.is_contiguous() and scales.is_contiguous()):
+            _dev(codes, rows * width, "codes")
+            _dev(scales, rows * blocks, "scales")
+        self.struct = ZsMx(codes.data_ptr(), scales.data_ptr(), rows, cols, code, 0)
+        self.ref = ctypes.byref(self.struct)
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
 
     @classmethod
     def empty(cls, rows, cols, format, device="cuda"):
@@ -1268,9 +1297,6 @@ class Mx:
                   scales.view(rows, cols // ZS_MX_BLOCK), cols, self.format)
 
 
-_MATRIX_TYPE = {**ZS_DTYPE, "torch.int16": 0, "torch.uint16": 0}
-
-
 def _matrix(x, name) -> ZsMatrix:
     """A GPU tensor as a zs_matrix: two dimensions (or one: a single row), the
     elements of a row side by side, rows any distance apart.  16-bit integers are
@@ -1278,21 +1304,23 @@ def _matrix(x, name) -> ZsMatrix:
     if not getattr(x, "is_cuda", False):
         raise ValueError("%s must be a GPU tensor (got %s)" % (name, getattr(x, "device",
                                                                              type(x))))
-    dtype = _MATRIX_TYPE.get(_type_name(x.dtype))
-    if dtype is None:
+    dtype = _matrix_type(x)
+    if dtype is None or dtype == _BYTES:
         raise TypeError("%s: %s is not bfloat16, float16 or float32" % (name, x.dtype))
-    if x.dim() == 1:
-        rows, cols, step, ld = 1, x.shape[0], x.stride(0), x.shape[0]
-    elif x.dim() == 2:
-        (rows, cols), (ld, step) = x.shape, x.stride()
+    shape, strides = x.shape, x.stride()
+    if len(shape) == 2:
+        (rows, cols), (ld, step) = shape, strides
         if rows <= 1:
             ld = cols
+    elif len(shape) == 1:
+        rows, cols, step = 1, shape[0], strides[0]
+        ld = cols
     else:
-        raise ValueError("%s must have one or two dimensions, not %d" % (name, x.dim()))
-    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        raise ValueError("%s must have one or two dimensions, not %d" % (name, len(shape)))
+    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError("%s: a row's elements must lie side by side and rows apart (strides %s)"
-                         % (name, tuple(x.stride())))
-    return ZsMatrix(x.data_ptr(), rows, cols, max(ld, cols), dtype, 0)
+                         % (name, tuple(strides)))
+    return ZsMatrix(x.data_ptr(), rows, cols, ld if ld > cols else cols, dtype, 0)
 
 
 def mx_workspace(device="cuda"):
@@ -1301,20 +1329,32 @@ def mx_workspace(device="cuda"):
     return _zeroed(ZS_MX_WORKSPACE_BYTES, device)
 
 
-def _held(x, name) -> ZsMx:
+def _held(x, name):
     if not isinstance(x, Mx):
         raise TypeError("%s: expected an Mx, got %r" % (name, type(x)))
-    return x.struct
+    return x.ref
 
 
-def _mx_call(name, tensors, workspace, args, stream, check) -> int:
-    """Enqueue a call of the microscaled formats on tensors of one device."""
-    index = _same_device([*tensors, workspace])
+def _mx_ready(name, held, first, second=None, workspace=None):
+    """Refuse buffers of several devices or of one that is not current, and a
+    workspace that belongs to a graph; the workspace's address."""
+    index = held.index
+    if first.get_device() != index if not isinstance(first, Mx) else first.index != index:
+        raise ValueError("%s: buffers on different devices" % name)
+    if second is not None and second.get_device() != index:
+        raise ValueError("%s: buffers on different devices" % name)
     _on_device(index)
-    if _made_in_capture(workspace):
+    if workspace is None:
+        return None
+    if getattr(workspace, "made_in_capture", False):
         _graph_only(name)
-    rc = getattr(load_library(), name)(*args, _stream_handle(stream))
-    if check and rc != ZS_OK:
+    if not isinstance(workspace, int) and workspace.get_device() not in (index, -1):
+        raise ValueError("%s: buffers on different devices" % name)
+    return _dev(workspace, ZS_MX_WORKSPACE_BYTES, "workspace")
+
+
+def _mx_done(rc, name, check) -> int:
+    if rc != ZS_OK and check:
         raise ZsError(rc, name)
     return rc
 
@@ -1322,49 +1362,53 @@ def _mx_call(name, tensors, workspace, args, stream, check) -> int:
 def zs_mx_quantize(x, out, stream=None, check=True) -> int:
     """Quantise the matrix x (bf16, fp16 or fp32) into the blocks of ``out``, an Mx
     of its size."""
-    return _mx_call("zs_mx_quantize", (x, out), None,
-                    (ctypes.byref(_matrix(x, "x")), ctypes.byref(_held(out, "out"))), stream,
-                    check)
+    m, ref = _matrix(x, "x"), _held(out, "out")
+    _mx_ready("zs_mx_quantize", out, x)
+    rc = load_library().zs_mx_quantize(ctypes.byref(m), ref, _stream_handle(stream))
+    return _mx_done(rc, "zs_mx_quantize", check)
 
 
 def zs_mx_dequantize(x, out, stream=None, check=True) -> int:
     """Write the values of an Mx into a matrix of its size (bf16, fp16 or fp32)."""
-    return _mx_call("zs_mx_dequantize", (x, out), None,
-                    (ctypes.byref(_held(x, "x")), ctypes.byref(_matrix(out, "out"))), stream,
-                    check)
-
-
-def _mx_space(workspace):
-    return None if workspace is None else _dev(workspace, ZS_MX_WORKSPACE_BYTES, "workspace")
+    ref, m = _held(x, "x"), _matrix(out, "out")
+    _mx_ready("zs_mx_dequantize", x, out)
+    rc = load_library().zs_mx_dequantize(ref, ctypes.byref(m), _stream_handle(stream))
+    return _mx_done(rc, "zs_mx_dequantize", check)
 
 
 def zs_mx_linear(x, w, y, stream=None, workspace=None, check=True) -> int:
     """y [M, N] = x [M, K] w^T for a bf16 x and an Mx w [N, K]; y is bf16 or fp32.
     With a ``workspace`` (mx_workspace) a product of few output tiles splits its
     sum over more of the device."""
-    return _mx_call("zs_mx_linear", (x, w, y), workspace,
-                    (ctypes.byref(_matrix(x, "x")), ctypes.byref(_held(w, "w")),
-                     ctypes.byref(_matrix(y, "y")), _mx_space(workspace)), stream, check)
+    ref, mx, my = _held(w, "w"), _matrix(x, "x"), _matrix(y, "y")
+    space = _mx_ready("zs_mx_linear", w, x, y, workspace)
+    rc = load_library().zs_mx_linear(ctypes.byref(mx), ref, ctypes.byref(my), space,
+                                     _stream_handle(stream))
+    return _mx_done(rc, "zs_mx_linear", check)
 
 
 def zs_mx_product(x, w, y, stream=None, workspace=None, check=True) -> int:
     """zs_mx_linear of an x that is an Mx itself."""
-    return _mx_call("zs_mx_product", (x, w, y), workspace,
-                    (ctypes.byref(_held(x, "x")), ctypes.byref(_held(w, "w")),
-                     ctypes.byref(_matrix(y, "y")), _mx_space(workspace)), stream, check)
+    ref, refx, my = _held(w, "w"), _held(x, "x"), _matrix(y, "y")
+    space = _mx_ready("zs_mx_product", w, x, y, workspace)
+    rc = load_library().zs_mx_product(refx, ref, ctypes.byref(my), space, _stream_handle(stream))
+    return _mx_done(rc, "zs_mx_product", check)
 
 
 def zs_mx_linear_dgrad(dy, w, dx, stream=None, workspace=None, check=True) -> int:
     """dx [M, K] = dy [M, N] w for a bf16 dy and an Mx w [N, K]; dx is bf16 or fp32."""
-    return _mx_call("zs_mx_linear_dgrad", (dy, w, dx), workspace,
-                    (ctypes.byref(_matrix(dy, "dy")), ctypes.byref(_held(w, "w")),
-                     ctypes.byref(_matrix(dx, "dx")), _mx_space(workspace)), stream, check)
+    ref, my, mx = _held(w, "w"), _matrix(dy, "dy"), _matrix(dx, "dx")
+    space = _mx_ready("zs_mx_linear_dgrad", w, dy, dx, workspace)
+    rc = load_library().zs_mx_linear_dgrad(ctypes.byref(my), ref, ctypes.byref(mx), space,
+                                           _stream_handle(stream))
+    return _mx_done(rc, "zs_mx_linear_dgrad", check)
 
 
 def zs_mx_linear_wgrad(dy, x, dw, add=False, stream=None, workspace=None, check=True) -> int:
     """dw [N, K] = dy [M, N]^T x for a bf16 dy and the activation x [M, K] kept as an
     Mx; dw is bf16 (a partial of the step) or fp32, where ``add`` adds to it."""
-    return _mx_call("zs_mx_linear_wgrad", (dy, x, dw), workspace,
-                    (ctypes.byref(_matrix(dy, "dy")), ctypes.byref(_held(x, "x")),
-                     ctypes.byref(_matrix(dw, "dw")), int(bool(add)), _mx_space(workspace)),
-                    stream, check)
+    ref, my, mw = _held(x, "x"), _matrix(dy, "dy"), _matrix(dw, "dw")
+    space = _mx_ready("zs_mx_linear_wgrad", x, dy, dw, workspace)
+    rc = load_library().zs_mx_linear_wgrad(ctypes.byref(my), ref, ctypes.byref(mw),
+                                           1 if add else 0, space, _stream_handle(stream))
+    return _mx_done(rc, "zs_mx_linear_wgrad", check)

@@ -727,7 +727,8 @@ struct Scales8 {
 // of a row and a column per instruction, at four times the rate of bf16.  A lane holds
 // a block of 32, so its scale is one byte, taken from a word of four by number.
 template <int BI, int BJ, int WI, int WJ, int KG>
-__global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArgs a) {
+__global__ __launch_bounds__(WI *WJ *KG *kWave, BI *BJ >= WI * WJ * 16384 ? 1 : 2) void
+mx_tile_fp4(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     constexpr int P_BYTES = BI * 128, Q_BYTES = BJ * 128;
@@ -736,8 +737,9 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
     // does not wait for what is on its way into the other
     __shared__ __attribute__((aligned(128))) char all0[KG][P_BYTES + Q_BYTES];
     __shared__ __attribute__((aligned(128))) char all1[KG][P_BYTES + Q_BYTES];
-    __shared__ uint64_t all_scales0[KG][NT];
-    __shared__ uint64_t all_scales1[KG][NT];
+    constexpr int SC = (BI + BJ + NT - 1) / NT;  // rows whose scales a thread takes
+    __shared__ uint64_t all_scales0[KG][SC * NT];
+    __shared__ uint64_t all_scales1[KG][SC * NT];
 
     const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
     const int tid = threadIdx.x % NT, lane = tid % kWave;
@@ -761,10 +763,13 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
     // a wave's chunk k: eight rows, lane / 8 the row, lane % 8 the place in it
     const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row & 7);
     const uint32_t p_off = (uint32_t)row * row_bytes + (uint32_t)chunk * 16u;
-    static_assert(NT >= BI + BJ, "a thread for the scales of each row");
-    const uint8_t *my_scales =
-        tid < BI ? a.px.scales + (int64_t)min(i0 + tid, a.I - 1) * nb
-                 : a.q.scales + (int64_t)min(j0 + tid - BI, a.J - 1) * nb;
+    const uint8_t *my_scales[SC];
+#pragma unroll
+    for (int c = 0; c < SC; ++c) {
+        const int at = c * NT + tid;
+        my_scales[c] = at < BI ? a.px.scales + (int64_t)min(i0 + at, a.I - 1) * nb
+                               : a.q.scales + (int64_t)min(j0 + at - BI, a.J - 1) * nb;
+    }
 
     auto fetch = [&](char *lds, int step) {
         const int block = (first + step) * kStep4Blocks;
@@ -780,10 +785,19 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
             dma16(q_buf, lds + P_BYTES + (k * (NT / 8) + wave * 8) * 128,
                   off + (uint32_t)(k * (NT / 8)) * row_bytes);
     };
+    struct Scales {
+        Scales8 of[SC];
+    };
     auto fetch_scales = [&](int step) {
-        Scales8 s;
-        s.load(my_scales, (first + step) * kStep4Blocks, nb);
+        Scales s;
+#pragma unroll
+        for (int c = 0; c < SC; ++c)
+            s.of[c].load(my_scales[c], (first + step) * kStep4Blocks, nb);
         return s;
+    };
+    auto put_scales = [&](uint64_t *to, const Scales &s) {
+#pragma unroll
+        for (int c = 0; c < SC; ++c) to[c * NT + tid] = s.of[c].value();
     };
 
     f32x16 acc[FJ][FI];
@@ -824,23 +838,23 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
 
     if (steps > 0) {
         fetch(lds0, 0);
-        scales0[tid] = fetch_scales(0).value();
+        put_scales(scales0, fetch_scales(0));
     }
     // two steps a turn: a split ends with a whole turn, or with the row, past which all is 0
 #pragma unroll 1
     for (int step = 0; step < steps; step += 2) {
         stage_ready<0>();
         fetch(lds1, step + 1);
-        Scales8 s = fetch_scales(step + 1);
+        Scales s = fetch_scales(step + 1);
         __builtin_amdgcn_sched_barrier(0);
         multiply(lds0, scales0);
-        scales1[tid] = s.value();
+        put_scales(scales1, s);
         stage_ready<0>();
         fetch(lds0, step + 2);
         s = fetch_scales(step + 2);
         __builtin_amdgcn_sched_barrier(0);
         multiply(lds1, scales1);
-        scales0[tid] = s.value();
+        put_scales(scales0, s);
     }
     if (KG > 1) stage_ready<0>();
     if (join_groups<KG>(acc, all0[0], all1[0], (int)sizeof(all0), BI * BJ * 4, group, wave, lane))

@@ -233,11 +233,8 @@ class FakeMatrix:
     def __init__(self, shape, strides, dtype="torch.bfloat16"):
         self.shape, self._s, self.dtype = shape, strides, dtype
 
-    def dim(self):
-        return len(self.shape)
-
-    def stride(self, i=None):
-        return self._s if i is None else self._s[i]
+    def stride(self):
+        return self._s
 
     def data_ptr(self):
         return A
