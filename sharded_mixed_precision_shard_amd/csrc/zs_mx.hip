@@ -27,7 +27,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Vectors at any address that suits their elements.
 struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
-struct __attribute__((packed, aligned(2))) Any8 { uint64_t v; };
 
 __device__ __forceinline__ float scale_of(uint32_t b) { return __uint_as_float(b << 23); }
 
@@ -245,12 +244,14 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize(MxCastArgs a) {
 constexpr int kStep = 64;  // c's per step: two blocks of a stored row
 
 // A tile in LDS holds bf16, kStep c's of B rows.  Row-major (c along a row):
-// 128 bytes a row, its eight 16-byte chunks in an order that the row's number
-// permutes, so that the 32 rows of a fragment read spread over the banks.
+// 128 bytes a row, half of the banks, its eight 16-byte chunks in an order that the row's
+// number permutes: any 16 neighbouring rows have a chunk in each of the 16 places, so the
+// reads of a fragment find no bank busy (permuted by row & 7 half of the LDS cycles of the 7B
+// products were conflicts).
 // Column-major (c a row of B elements): the 64-byte chunks of a row permuted by
 // c for the same reason.
 __device__ __forceinline__ int at_rows(int row, int chunk) {
-    return row * 128 + ((chunk ^ (row & 7)) << 4);
+    return row * 128 + ((chunk ^ (row >> 1 & 7)) << 4);
 }
 template <int B>
 __device__ __forceinline__ int at_cols(int c, int byte) {
@@ -395,26 +396,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return bits(v);
 }
 
-// Four values of out[i, j ..], added to what is there where the call says so.
-__device__ __forceinline__ void put4(const MxProductArgs &a, int i, int j, f32x4 v) {
+// 16 bytes of out from [i, j] on, added to what is there where the call says so.
+__device__ __forceinline__ void put16(const MxProductArgs &a, int i, int j, u32x4 v) {
     if (i >= a.I || j >= a.J) return;
     const int64_t at = (int64_t)i * a.ldo + j;
     if (a.out_f32) {
         float *o = (float *)a.out + at;
         if (j + 4 <= a.J) {
-            if (a.add) v += __builtin_bit_cast(f32x4, ((const Any16 *)o)->v);
-            ((Any16 *)o)->v = __builtin_bit_cast(u32x4, v);
+            if (a.add) {
+                const u32x4 old = ((const Any16 *)o)->v;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = __float_as_uint(__uint_as_float(old[e]) + __uint_as_float(v[e]));
+            }
+            ((Any16 *)o)->v = v;
         } else {
-            for (int e = 0; e < 4 && j + e < a.J; ++e) o[e] = a.add ? o[e] + v[e] : v[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (j + e < a.J) o[e] = (a.add ? o[e] : 0.0f) + __uint_as_float(v[e]);
         }
     } else {
         uint16_t *o = (uint16_t *)a.out + at;
-        const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
-        if (j + 4 <= a.J) {
-            ((Any8 *)o)->v = (uint64_t)hi << 32 | lo;
+        if (j + 8 <= a.J) {
+            ((Any16 *)o)->v = v;
         } else {
-            for (int e = 0; e < 4 && j + e < a.J; ++e)
-                o[e] = (uint16_t)((e < 2 ? lo : hi) >> (16 * (e % 2)));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (j + e < a.J) o[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
         }
     }
 }
@@ -534,19 +542,18 @@ __device__ __forceinline__ bool join_groups(f32x16 (&acc)[FJ][FI], char *a, char
                     for (int e = 0; e < 4; ++e) acc[j][i][4 * r + e] += v[e];
                 }
     }
+    __syncthreads();  // the waves of the first group, for a and b to be written again
     return true;
 }
 
-// The end of a tile: its sums go out, or to the workspace, where the last of the splits
-// adds them.
+// The end of a tile: its sums go out, or to the workspace, where another split finds them.
+// `stage` is 4 KB of LDS per wave that nothing reads any more.
 template <int BI, int BJ, int WI, int WJ>
 __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
                                             f32x16 (&acc)[BJ / WJ / 32][BI / WI / 32],
                                             int tile, int split, int i0, int j0, int wi, int wj,
-                                            int wave, int lane, uint32_t *shared) {
+                                            int wave, int lane, uint32_t *shared, char *stage) {
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
-    // lane: i = lane % 32, and for each r four j's from 8 r + 4 (lane / 32)
-    const int li = wi + lane % 32, lj = wj + lane / 32 * 4;
     // Splits are joined two by two: of splits [s, s + n) and [s + n, s + 2 n) the one that is
     // done first leaves its sums and ends, the other adds them to its own and goes on with
     // both.  The tree is the same every time and an addition's two sides may change places,
@@ -585,15 +592,48 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
                 }
         __syncthreads();  // `shared` is free again
     }
+    // A lane holds four neighbours of one row of out.  Through LDS a wave's 32 rows leave in
+    // stretches of 64 or 128 bytes (bf16; 128 in fp32), 16 bytes a lane.
+    char *mine = stage + wave * 4096;
+    const int i = lane % 32, half = lane / 32, row = lane / 8, chunk = lane % 8;
+    constexpr int PAIR = FJ % 2 == 0 ? 2 : 1;  // fragments side by side in a row of bf16
 #pragma unroll
-    for (int j = 0; j < FJ; ++j)
+    for (int f = 0; f < FI; ++f) {
+        if (a.out_f32) {
 #pragma unroll
-        for (int i = 0; i < FI; ++i)
+            for (int j = 0; j < FJ; ++j) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                put4(a, i0 + li + 32 * i, j0 + lj + 32 * j + 8 * r,
-                     f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1], acc[j][i][4 * r + 2],
-                           acc[j][i][4 * r + 3]});
+                for (int r = 0; r < 4; ++r)
+                    *(f32x4 *)(mine + at_rows(i, 2 * r + half)) =
+                        f32x4{acc[j][f][4 * r], acc[j][f][4 * r + 1], acc[j][f][4 * r + 2],
+                              acc[j][f][4 * r + 3]};
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    put16(a, i0 + wi + 32 * f + 8 * k + row, j0 + wj + 32 * j + 4 * chunk,
+                          *(const u32x4 *)(mine + at_rows(8 * k + row, chunk)));
+                __builtin_amdgcn_wave_barrier();
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < FJ; j += PAIR) {
+#pragma unroll
+                for (int e = 0; e < PAIR; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        *(uint2 *)(mine + at_rows(i, 4 * e + r) + 8 * half) =
+                            uint2{pack_bf16(acc[j + e][f][4 * r], acc[j + e][f][4 * r + 1]),
+                                  pack_bf16(acc[j + e][f][4 * r + 2], acc[j + e][f][4 * r + 3])};
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (PAIR == 2 || chunk < 4)
+                        put16(a, i0 + wi + 32 * f + 8 * k + row, j0 + wj + 32 * j + 8 * chunk,
+                              *(const u32x4 *)(mine + at_rows(8 * k + row, chunk)));
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+    }
 }
 
 // The steps that each wave group of a split takes; past the last c all reads as 0.
@@ -677,10 +717,11 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave) void mx_tile(MxProductArgs a) {
         if (more) store((step + 1) % 2);
     }
 
-    if (KG > 1) __syncthreads();
+    __shared__ uint32_t shared;
+    __syncthreads();
     if (join_groups<KG>(acc, all[0], all[0], (int)sizeof(all), BI * BJ * 4, group, wave, lane))
-        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
-                                    (uint32_t *)all);
+        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, &shared,
+                                    all[0]);
 }
 
 // ---------------------------------------------- products of two fp4 operands
@@ -761,7 +802,7 @@ mx_tile_fp4(MxProductArgs a) {
     const auto q_buf = buffer_of(a.q.codes + (int64_t)j0 * row_bytes,
                                  (uint32_t)min(a.J - j0, BJ) * row_bytes);
     // a wave's chunk k: eight rows, lane / 8 the row, lane % 8 the place in it
-    const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row & 7);
+    const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row >> 1 & 7);
     const uint32_t p_off = (uint32_t)row * row_bytes + (uint32_t)chunk * 16u;
     const uint8_t *my_scales[SC];
 #pragma unroll
@@ -771,8 +812,15 @@ mx_tile_fp4(MxProductArgs a) {
                                : a.q.scales + (int64_t)min(j0 + at - BI, a.J - 1) * nb;
     }
 
+    // tiles begin at different steps: the rows of wide operands lie a power of two apart, and
+    // workgroups that read the same columns at a time would meet on few of the L2's channels
+    const int turns = (steps + 1) / 2 * 2, skew = turns > 0 ? (ti + tj) % 16 * 2 % turns : 0;
+    auto block_of = [&](int step) {
+        step += skew;
+        return (first + (step >= turns ? step - turns : step)) * kStep4Blocks;
+    };
     auto fetch = [&](char *lds, int step) {
-        const int block = (first + step) * kStep4Blocks;
+        const int block = block_of(step);
         // blocks past the row's end read as zero codes (all of the address is in the lane's
         // offset, which is what the size is compared with)
         const uint32_t off = block + chunk < nb ? p_off + (uint32_t)block * 16u : kNowhere;
@@ -792,7 +840,7 @@ mx_tile_fp4(MxProductArgs a) {
         Scales s;
 #pragma unroll
         for (int c = 0; c < SC; ++c)
-            s.of[c].load(my_scales[c], (first + step) * kStep4Blocks, nb);
+            s.of[c].load(my_scales[c], block_of(step), nb);
         return s;
     };
     auto put_scales = [&](uint64_t *to, const Scales &s) {
@@ -818,7 +866,7 @@ mx_tile_fp4(MxProductArgs a) {
         // instruction
 #define ZS_MX_QUARTER(S)                                                                       \
     {                                                                                          \
-        const int at = ((4 * h + S) ^ (r & 7)) << 4;                                           \
+        const int at = ((4 * h + S) ^ (r >> 1 & 7)) << 4;                                           \
         i32x8 pf[FI], qf[FJ];                                                                  \
         _Pragma("unroll") for (int i = 0; i < FI; ++i) pf[i] =                                 \
             codes4(*(const u32x4 *)(p + i * 4096 + at));                                       \
@@ -856,10 +904,10 @@ mx_tile_fp4(MxProductArgs a) {
         multiply(lds1, scales1);
         put_scales(scales0, s);
     }
-    if (KG > 1) stage_ready<0>();
+    stage_ready<0>();
     if (join_groups<KG>(acc, all0[0], all1[0], (int)sizeof(all0), BI * BJ * 4, group, wave, lane))
         finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
-                                    (uint32_t *)all_scales0);
+                                    (uint32_t *)all_scales0, all0[0]);
 }
 
 // ------------------------------------- bf16 against blocks, rows in full chunks
@@ -899,7 +947,7 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductAr
 
     const uint32_t row_bytes = (uint32_t)a.ldp * 2u;
     const auto p_buf = buffer_of(a.p + (int64_t)i0 * a.ldp, (uint32_t)min(a.I - i0, BI) * row_bytes);
-    const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row & 7);
+    const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row >> 1 & 7);
     const uint32_t p_off = (uint32_t)row * row_bytes + (uint32_t)chunk * 16u;
     const uint8_t *codes[FJ];
     const uint8_t *scales[FJ];
@@ -1046,7 +1094,7 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductAr
     stage_ready<0>();
     if (join_groups<KG>(acc, all0[0], all1[0], (int)sizeof(all0), BI * BJ * 4, group, wave, lane))
         finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
-                                    (uint32_t *)all3);
+                                    (uint32_t *)all3, all0[0]);
 }
 
 // dx = dy w and dw = dy^T x: the stored operand's rows run along the output, so a fragment
@@ -1094,7 +1142,7 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
         p_off = (uint32_t)c * p_row + (uint32_t)byte;
     } else {
         const int row = wave * 8 + lane / 8;
-        chunk = (lane % 8) ^ (row & 7);
+        chunk = (lane % 8) ^ (row >> 1 & 7);
         p_off = (uint32_t)row * p_row + (uint32_t)chunk * 16u;
     }
     auto fetch = [&](char *lds, int step) {
@@ -1141,17 +1189,32 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
         b.scale = __builtin_amdgcn_raw_buffer_load_b8(scales, off, 0, 0);
         return b;
     };
+    // The lanes that write together hold the blocks of two rows: each block's four chunks go
+    // out in an order of its own, so that the banks differ.
+    const int turn0 = qb >> 2 & 1, turn1 = qc & 1;
     auto put_block = [&](char *lds, const Block &b) {
         if (ROW * kStep < NT && qc >= kStep) return;
         const float s = scale_of(b.scale);
+        // words of the chunks w ^ turn
+        uint32_t c[4][W];
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                auto word = [&](int k) { return b.v[(k * W + e) / 4][(k * W + e) % 4]; };
+                const uint32_t x = turn0 ? word(w ^ 1) : word(w);
+                const uint32_t y = turn0 ? word(w ^ 3) : word(w ^ 2);
+                c[w][e] = turn1 ? y : x;
+            }
+        const int turn = turn0 | turn1 << 1;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             u32x4 v;
             if constexpr (F8)
-                v = widen_fp8(b.v[w / 2][w % 2 * 2], b.v[w / 2][w % 2 * 2 + 1], s);
+                v = widen_fp8(c[w][0], c[w][1], s);
             else
-                v = widen_fp4(b.v[0][w], s);
-            *(u32x4 *)(lds + at_cols<BJ>(qc, qb * 64 + w * 16)) = v;
+                v = widen_fp4(c[w][0], s);
+            *(u32x4 *)(lds + at_cols<BJ>(qc, qb * 64 + (w ^ turn) * 16)) = v;
         }
     };
 
@@ -1221,7 +1284,7 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
     if (join_groups<KG>(acc, all_p0[0], all_p1[0], (int)sizeof(all_p0), BI * BJ * 4, group, wave,
                         lane))
         finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
-                                    (uint32_t *)all_q0);
+                                    (uint32_t *)all_q0, all_p0[0]);
 }
 
 // ------------------------------------------------------- products of few rows
