@@ -248,19 +248,20 @@ constexpr int kStep = 64;  // c's per step: two blocks of a stored row
 // number permutes: any 16 neighbouring rows have a chunk in each of the 16 places, so the
 // reads of a fragment find no bank busy (permuted by row & 7 half of the LDS cycles of the 7B
 // products were conflicts).
-// Column-major (c a row of B elements): the 64-byte chunks of a row permuted by
-// c for the same reason.
+// Column-major (c a row of B elements): the 64-byte chunks of a row are permuted by c, and
+// the 16 bytes inside each, too.  Four rows' 64 bytes, which a transposing read takes, then lie
+// in different banks, and so do the pieces that lanes of four rows and blocks write together.
 __device__ __forceinline__ int at_rows(int row, int chunk) {
     return row * 128 + ((chunk ^ (row >> 1 & 7)) << 4);
 }
 template <int B>
 __device__ __forceinline__ int at_cols(int c, int byte) {
     if constexpr (B >= 256)
-        return c * (B * 2) + (byte ^ ((c & 7) << 6));
+        return c * (B * 2) + (byte ^ ((c & 7) << 6) ^ ((c & 3) << 4));
     else if constexpr (B == 128)
-        return c * (B * 2) + (byte ^ ((c & 3) << 6));
+        return c * (B * 2) + (byte ^ ((c & 3) << 6) ^ ((c & 3) << 4));
     else
-        return c * (B * 2) + (byte ^ (((c >> 1) & 1) << 6));
+        return c * (B * 2) + (byte ^ ((c >> 1 & 1) << 6) ^ ((c >> 1 & 3) << 4));
 }
 
 // The 8 c's of a 32x32x16 fragment that a lane holds: c = 16 s + 8 (lane / 32) ..
@@ -1168,7 +1169,9 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
     };
 
     const uint32_t q_row = (uint32_t)a.q.nb;
-    const int qc = tid / ROW, qb = tid % ROW;  // the thread's block of a step
+    // the thread's block of a step: neighbours take up to four of a row
+    constexpr int SIDE = ROW < 4 ? ROW : 4;
+    const int qc = tid / SIDE % kStep, qb = tid % SIDE + tid / (SIDE * kStep) * SIDE;
     struct Block {
         u32x4 v[W];
         uint32_t scale;
@@ -1189,32 +1192,17 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
         b.scale = __builtin_amdgcn_raw_buffer_load_b8(scales, off, 0, 0);
         return b;
     };
-    // The lanes that write together hold the blocks of two rows: each block's four chunks go
-    // out in an order of its own, so that the banks differ.
-    const int turn0 = qb >> 2 & 1, turn1 = qc & 1;
     auto put_block = [&](char *lds, const Block &b) {
-        if (ROW * kStep < NT && qc >= kStep) return;
+        if (ROW * kStep < NT && qb >= ROW) return;
         const float s = scale_of(b.scale);
-        // words of the chunks w ^ turn
-        uint32_t c[4][W];
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-#pragma unroll
-            for (int e = 0; e < W; ++e) {
-                auto word = [&](int k) { return b.v[(k * W + e) / 4][(k * W + e) % 4]; };
-                const uint32_t x = turn0 ? word(w ^ 1) : word(w);
-                const uint32_t y = turn0 ? word(w ^ 3) : word(w ^ 2);
-                c[w][e] = turn1 ? y : x;
-            }
-        const int turn = turn0 | turn1 << 1;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             u32x4 v;
             if constexpr (F8)
-                v = widen_fp8(c[w][0], c[w][1], s);
+                v = widen_fp8(b.v[w / 2][w % 2 * 2], b.v[w / 2][w % 2 * 2 + 1], s);
             else
-                v = widen_fp4(c[w][0], s);
-            *(u32x4 *)(lds + at_cols<BJ>(qc, qb * 64 + (w ^ turn) * 16)) = v;
+                v = widen_fp4(b.v[0][w], s);
+            *(u32x4 *)(lds + at_cols<BJ>(qc, qb * 64 + w * 16)) = v;
         }
     };
 
@@ -1239,6 +1227,9 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
                 for (int i = 0; i < FI; ++i)
                     acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[j], pf[i], acc[j][i], 0,
                                                                         0, 0);
+            // the reads of a quarter stay in it: hoisted, they would take the registers of the
+            // block two steps ahead (seven spilled, 7B wgrad 851 us instead of 675)
+            if (F8) __builtin_amdgcn_sched_barrier(0);
         }
     };
 
