@@ -324,12 +324,28 @@ struct PlainStage {
             r[k] = v;
         }
     }
-    __device__ __forceinline__ void store(char *lds, int tid) {
+    // The same where every c of the step and the one after it is inside, and rows >= 8: what
+    // lies past the rows is read from inside the matrix, as part of sums that nobody keeps.
+    __device__ __forceinline__ void load_inside(const uint16_t *p, int64_t ld, int first, int rows,
+                                                int c0, int tid) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int q = k * NT + tid;
+            int64_t at;
+            if constexpr (COLS)
+                at = (int64_t)(c0 + q / (B / 8)) * ld + min(first + q % (B / 8) * 8, rows - 1);
+            else
+                at = (int64_t)min(first + q / 8, rows - 1) * ld + c0 + q % 8 * 8;
+            r[k] = ((const Any16 *)(p + at))->v;
+        }
+    }
+    // Zeros go to LDS where `in` is false.
+    __device__ __forceinline__ void store(char *lds, int tid, bool in = true) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int q = k * NT + tid;
             const int at = COLS ? at_cols<B>(q / (B / 8), q % (B / 8) * 16) : at_rows(q / 8, q % 8);
-            *(u32x4 *)(lds + at) = r[k];
+            *(u32x4 *)(lds + at) = in ? r[k] : u32x4{0, 0, 0, 0};
         }
     }
 };
@@ -370,12 +386,30 @@ struct HeldStage {
             }
         }
     }
-    __device__ __forceinline__ void store(char *lds, int tid) {
+    __device__ __forceinline__ void load_inside(const MxHeld &x, int first, int rows, int c0,
+                                                int tid) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int q = min(k * NT + tid, kUnits - 1);
+            int64_t at;
+            if constexpr (COLS)
+                at = (int64_t)(c0 + q / (B / kMxBlock)) * x.nb +
+                     min((int64_t)(first / kMxBlock + q % (B / kMxBlock)), x.nb - 1);
+            else
+                at = (int64_t)min(first + q / 2, rows - 1) * x.nb + c0 / kMxBlock + q % 2;
+            const u32x4 *codes = (const u32x4 *)x.codes + at * (F8 ? 2 : 1);
+            r[k][0] = codes[0];
+            if constexpr (F8) r[k][1] = codes[1];
+            scale[k] = x.scales[at];
+        }
+    }
+    // Numbers of no consequence go to LDS where `in` is false (the other operand's are 0).
+    __device__ __forceinline__ void store(char *lds, int tid, bool in = true) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int q = k * NT + tid;
             if (kUnits % NT != 0 && q >= kUnits) continue;
-            const float s = scale_of(scale[k]);
+            const float s = scale_of(in ? scale[k] : 0u);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 u32x4 v;
@@ -647,7 +681,7 @@ __device__ __forceinline__ int group_steps(const MxProductArgs &a, int depth, in
 // instruction takes Q's rows as its rows and P's as its columns: a lane then
 // holds four neighbouring j's of one i, and stores them together.
 template <int BI, int BJ, int WI, int WJ, int KG, int LEFT, int RIGHT>
-__global__ __launch_bounds__(WI *WJ *KG *kWave) void mx_tile(MxProductArgs a) {
+__global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     constexpr bool PC = LEFT == kLeftCols, QC = (RIGHT & kRightCols) != 0;
@@ -663,40 +697,18 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave) void mx_tile(MxProductArgs a) {
     tile_of(blockIdx.x / a.splits, a.tiles_i, a.tiles_j, &ti, &tj);
     const int tile = tj * a.tiles_i + ti, i0 = ti * BI, j0 = tj * BJ;
     const int wi = wave % WI * (BI / WI), wj = wave / WI * (BJ / WJ);
+    // The last step, whole or not, is taken first and element by element; the others have all
+    // of their c's inside, and no branches.
+    const int full = a.C > 0 ? (a.C - 1) / kStep : 0;
     const int first = (split * KG + group) * a.split_steps;
-    const int steps = group_steps<KG>(a, kStep, split);
+    const int steps = min(full - split * KG * a.split_steps, a.split_steps);
 
     f32x16 acc[FJ][FI];
 #pragma unroll
     for (int j = 0; j < FJ; ++j)
 #pragma unroll
         for (int i = 0; i < FI; ++i) acc[j][i] = f32x16{};
-
-    std::conditional_t<P_HELD, HeldStage<BI, NT, false, LEFT == kLeftFp8>,
-                       PlainStage<BI, NT, PC>> ps;
-    HeldStage<BJ, NT, QC, (RIGHT & kRightFp8) != 0> qs;
-    auto load = [&](int step) {
-        const int c0 = (first + step) * kStep;
-        if constexpr (P_HELD)
-            ps.load(a.px, i0, a.I, c0, a.C, tid);
-        else
-            ps.load(a.p, a.ldp, i0, a.I, c0, a.C, tid);
-        qs.load(a.q, j0, a.J, c0, a.C, tid);
-    };
-    auto store = [&](int buffer) {
-        char *p = lds + buffer * (P_BYTES + Q_BYTES);
-        ps.store(p, tid);
-        qs.store(p + P_BYTES, tid);
-    };
-    if (steps > 0) {
-        load(0);
-        store(0);
-    }
-    for (int step = 0; step < steps; ++step) {
-        const bool more = step + 1 < steps;
-        if (more) load(step + 1);
-        __syncthreads();
-        const char *p = lds + step % 2 * (P_BYTES + Q_BYTES), *q = p + P_BYTES;
+    auto multiply = [&](const char *p, const char *q) {
 #pragma unroll
         for (int s = 0; s < kStep / 16; ++s) {
             bf16x8 pf[FI], qf[FJ];
@@ -715,7 +727,51 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave) void mx_tile(MxProductArgs a) {
                     acc[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(qf[j], pf[i], acc[j][i], 0,
                                                                         0, 0);
         }
-        if (more) store((step + 1) % 2);
+    };
+
+    std::conditional_t<P_HELD, HeldStage<BI, NT, false, LEFT == kLeftFp8>,
+                       PlainStage<BI, NT, PC>> ps;
+    HeldStage<BJ, NT, QC, (RIGHT & kRightFp8) != 0> qs;
+    if (split == 0 && a.C > 0) {
+        const int c0 = group == 0 ? full * kStep : a.C;  // the other groups add zeros
+        if constexpr (P_HELD)
+            ps.load(a.px, i0, group == 0 ? a.I : 0, c0, a.C, tid);
+        else
+            ps.load(a.p, a.ldp, i0, a.I, c0, a.C, tid);
+        qs.load(a.q, j0, group == 0 ? a.J : 0, c0, a.C, tid);
+        ps.store(lds, tid);
+        qs.store(lds + P_BYTES, tid);
+        __syncthreads();
+        multiply(lds, lds + P_BYTES);
+        __syncthreads();
+    }
+    auto load = [&](int step) {
+        const int c0 = min(first + step, full - 1) * kStep;
+        if constexpr (P_HELD)
+            ps.load_inside(a.px, i0, a.I, c0, tid);
+        else if (PC && a.I < 8)
+            ps.load(a.p, a.ldp, i0, a.I, c0, a.C, tid);
+        else
+            ps.load_inside(a.p, a.ldp, i0, a.I, c0, tid);
+        qs.load_inside(a.q, j0, a.J, c0, tid);
+    };
+    auto store = [&](int step) {
+        char *p = lds + step % 2 * (P_BYTES + Q_BYTES);
+        const bool in = KG == 1 || first + step < full;
+        ps.store(p, tid, in);
+        qs.store(p + P_BYTES, tid, in);
+    };
+    if (steps > 0) {
+        load(0);
+        store(0);
+    }
+#pragma unroll 1
+    for (int step = 0; step < steps; ++step) {
+        load(step + 1);  // past the last step this reads the last one again
+        __syncthreads();
+        const char *p = lds + step % 2 * (P_BYTES + Q_BYTES);
+        multiply(p, p + P_BYTES);
+        store(step + 1);
     }
 
     __shared__ uint32_t shared;
@@ -1681,7 +1737,10 @@ hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &d
 template <int LEFT, int RIGHT>
 hipError_t choose_tile(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                        hipStream_t stream) {
-    if ((int64_t)a.I * a.J >= (int64_t)dev.cus * 128 * 128)
+    const int64_t out = (int64_t)a.I * a.J;
+    if (out >= (int64_t)dev.cus * 256 * 256 / 2)
+        return run_tile<256, 256, 2, 4, 1, LEFT, RIGHT>(a, workspace, dev, stream);
+    if (out >= (int64_t)dev.cus * 128 * 128)
         return run_tile<128, 128, 2, 2, 1, LEFT, RIGHT>(a, workspace, dev, stream);
     if (a.I > 64 && a.C >= kLong)
         return run_tile<128, 128, 2, 2, 2, LEFT, RIGHT>(a, workspace, dev, stream);

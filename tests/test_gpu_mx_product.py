@@ -416,3 +416,16 @@ def test_many_tiles(gpu, workspace, op, fmt, depth):
         case.check_equal(out)
         out.fill_(55.0)
         assert torch.equal(flat, before)
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 7, 8, 9])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_narrow_gradients(gpu, workspace, n, pad):
+    """dw of a few rows: dy's rows are shorter than a chunk."""
+    torch = gpu
+    for m, k in ((1, 40), (64, 33), (65, 100), (130, 64), (9001, 70)):
+        case = Case(torch, "wgrad", m, n, k, "fp8", True, m, pad=pad)
+        for space in (None, workspace):
+            _, out = case.out(torch.float32)
+            case.call(out, space)
+            case.check_equal(out)
