@@ -431,24 +431,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return bits(v);
 }
 
-// 16 bytes of out from [i, j] on, added to what is there where the call says so.
+// 16 bytes of out from [i, j] on, as far as there are.
 __device__ __forceinline__ void put16(const MxProductArgs &a, int i, int j, u32x4 v) {
     if (i >= a.I || j >= a.J) return;
     const int64_t at = (int64_t)i * a.ldo + j;
     if (a.out_f32) {
-        float *o = (float *)a.out + at;
+        uint32_t *o = (uint32_t *)a.out + at;
         if (j + 4 <= a.J) {
-            if (a.add) {
-                const u32x4 old = ((const Any16 *)o)->v;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    v[e] = __float_as_uint(__uint_as_float(old[e]) + __uint_as_float(v[e]));
-            }
             ((Any16 *)o)->v = v;
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (j + e < a.J) o[e] = (a.add ? o[e] : 0.0f) + __uint_as_float(v[e]);
+                if (j + e < a.J) o[e] = v[e];
         }
     } else {
         uint16_t *o = (uint16_t *)a.out + at;
@@ -460,6 +454,17 @@ __device__ __forceinline__ void put16(const MxProductArgs &a, int i, int j, u32x
                 if (j + e < a.J) o[e] = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
         }
     }
+}
+// The fp32 values there, zeros past the end.
+__device__ __forceinline__ u32x4 there(const MxProductArgs &a, int i, int j) {
+    u32x4 v = {0, 0, 0, 0};
+    if (i >= a.I || j >= a.J) return v;
+    const uint32_t *o = (const uint32_t *)a.out + (int64_t)i * a.ldo + j;
+    if (j + 4 <= a.J) return ((const Any16 *)o)->v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (j + e < a.J) v[e] = o[e];
+    return v;
 }
 
 // One value of out.
@@ -635,6 +640,18 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
 #pragma unroll
     for (int f = 0; f < FI; ++f) {
         if (a.out_f32) {
+            // what is there already, all of it on its way at a time (4096^3 151 us one after the
+            // other, 142 so)
+            u32x4 old[FJ][4];
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    old[j][k] = u32x4{0, 0, 0, 0};
+                    if (a.add)
+                        old[j][k] = there(a, i0 + wi + 32 * f + 8 * k + row,
+                                          j0 + wj + 32 * j + 4 * chunk);
+                }
 #pragma unroll
             for (int j = 0; j < FJ; ++j) {
 #pragma unroll
@@ -644,9 +661,16 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
                               acc[j][f][4 * r + 3]};
                 __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    put16(a, i0 + wi + 32 * f + 8 * k + row, j0 + wj + 32 * j + 4 * chunk,
-                          *(const u32x4 *)(mine + at_rows(8 * k + row, chunk)));
+                for (int k = 0; k < 4; ++k) {
+                    u32x4 v = *(const u32x4 *)(mine + at_rows(8 * k + row, chunk));
+                    if (a.add) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = __float_as_uint(__uint_as_float(old[j][k][e]) +
+                                                   __uint_as_float(v[e]));
+                    }
+                    put16(a, i0 + wi + 32 * f + 8 * k + row, j0 + wj + 32 * j + 4 * chunk, v);
+                }
                 __builtin_amdgcn_wave_barrier();
             }
         } else {
