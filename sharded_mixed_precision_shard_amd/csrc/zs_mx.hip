@@ -1621,8 +1621,28 @@ void plan(MxProductArgs *a, int bi, int bj, int groups, int depth, int turn, voi
     a->parts = (float *)((char *)workspace + kMxCounterBytes);
 }
 
-// Depth from which an output of few tiles is made in large ones all the same.
+// The size of the tiles, by the elements of out (cus of 256 in the figures below; in us, each
+// with the next smaller or larger choice).  Tiles of 256 x 256 from a tile per compute unit
+// on: bf16 by fp4, K = 4096, 4096 x 4096 107 against 138 in tiles of 128, 2048 x 4096 81 and 71;
+// dgrad 111 and 137, 91 and 72; fp4 48 and 60, 38 and 33; any strides 130 and 167, 115 and 89.
+constexpr int64_t kTile256 = 256 * 256;
+// Tiles of 128 x 128, more than a compute unit each, in one wave group; up to that many in two,
+// since a wave per SIMD hides little: dgrad 2048 x 4096 (512 tiles) 72 in one, 79 in two groups,
+// 1024 x 4096 (256) 45 and 41; fp4 33 and 36, 22 and 20; any strides 89 and 101, 56 and 52, and
+// 2001 x 3001 (384) 23 and 30.
+bool many_tiles(const MxProductArgs &a, const MxDevice &dev) {
+    return (int64_t)((a.I + 127) / 128) * ((a.J + 127) / 128) > dev.cus;
+}
+// Below that, tiles of 64 x 64 in several wave groups leave fewer sums to be joined through
+// memory: fp4 512 x 4096 16 in tiles of 128, 23 so, 256 x 4096 14 and 12; any strides 33 and 51, 27
+// and 26.
+constexpr int64_t kTile64 = 6 * 1024;
+// Long sums are worth large tiles all the same: any strides, 256 x 2048 of depth 16384 40 in
+// tiles of 128, 45 in tiles of 64, 256 x 4096 of depth 4096 27 and 26.
 constexpr int kLong = 8192;
+// Rows of w from which up to 64 rows of x take tiles of 128 of them instead of 64: 64 rows,
+// N = 28672 53 and 68 (fp4 38 and 45), N = 16384 24 and 21 (16 and 15).
+constexpr int64_t kWideRows = 96;
 
 dim3 grid_of(const MxProductArgs &a) {
     return dim3((uint32_t)((int64_t)a.tiles_i * a.tiles_j * a.splits));
@@ -1704,21 +1724,19 @@ hipError_t choose_few(const MxProductArgs &a, void *workspace, const MxDevice &d
     return run_few<LEFT, F8, 4, 1, 8>(a, workspace, dev, stream);
 }
 
+// Here one wave group is as good as two in tiles of 128 (512 x 4096 26 and 29, 1024 x 4096 39 and
+// 41): the codes' way through registers hides more.
 template <bool F8>
 hipError_t choose_rows(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                        hipStream_t stream) {
     const int64_t out = (int64_t)a.I * a.J;
-    if (out >= (int64_t)dev.cus * 256 * 256)
+    if (out >= kTile256 * dev.cus)
         return run_rows<256, 256, 2, 4, 1, F8>(a, workspace, dev, stream);
-    if (out >= (int64_t)dev.cus * 128 * 128)
-        return run_rows<128, 128, 2, 2, 1, F8>(a, workspace, dev, stream);
-    if (a.I <= 32 && a.J >= 64 * dev.cus)
-        return run_rows<32, 128, 1, 4, 1, F8>(a, workspace, dev, stream);
-    if (a.I <= 64 && a.J >= 64 * dev.cus)
-        return run_rows<64, 128, 1, 4, 1, F8>(a, workspace, dev, stream);
     if (a.I <= 32) return run_rows<32, 128, 1, 4, 2, F8>(a, workspace, dev, stream);
-    if (a.I > 64 && a.C >= kLong)
-        return run_rows<128, 128, 2, 2, 2, F8>(a, workspace, dev, stream);
+    if (a.I <= 64 && a.J >= kWideRows * dev.cus)
+        return run_rows<64, 128, 1, 4, 1, F8>(a, workspace, dev, stream);
+    if (out >= kTile64 * dev.cus || (a.I > 64 && a.C >= kLong))
+        return run_rows<128, 128, 2, 2, 1, F8>(a, workspace, dev, stream);
     return run_rows<64, 64, 2, 2, 2, F8>(a, workspace, dev, stream);
 }
 
@@ -1730,47 +1748,52 @@ hipError_t run_cols(MxProductArgs a, void *workspace, const MxDevice &dev, hipSt
     return hipGetLastError();
 }
 
+// The transposing reads make small tiles dear: 64 x 64 is for small and shallow outputs only
+// (dgrad 1024 x 768 of depth 768 9.6, in tiles of 128 10.6; wgrad 768 x 768 of depth 2048 17.5
+// and 17.7, of depth 8192 53 and 28; 1024 x 1024 of depth 4096 28 and 26).
+constexpr int64_t kTile64Cols = 4 * 1024;
+constexpr int kLongCols = 4096;
+
 template <bool PC, bool F8>
 hipError_t choose_cols(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                        hipStream_t stream) {
     const int64_t out = (int64_t)a.I * a.J;
-    if (out >= (int64_t)dev.cus * 256 * 256 / 2)
+    if (out >= kTile256 * dev.cus)
         return run_cols<256, 256, 2, 4, 1, PC, F8>(a, workspace, dev, stream);
-    if (out >= (int64_t)dev.cus * 128 * 128)
+    if (many_tiles(a, dev))
         return run_cols<128, 128, 2, 2, 1, PC, F8>(a, workspace, dev, stream);
-    if (a.C >= kLong) return run_cols<128, 128, 2, 2, 2, PC, F8>(a, workspace, dev, stream);
+    if (out >= kTile64Cols * dev.cus || a.C >= kLongCols)
+        return run_cols<128, 128, 2, 2, 2, PC, F8>(a, workspace, dev, stream);
     return run_cols<64, 64, 2, 2, 4, PC, F8>(a, workspace, dev, stream);
 }
 
 hipError_t choose_fp4(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                       hipStream_t stream) {
     const int64_t out = (int64_t)a.I * a.J;
-    if (out >= (int64_t)dev.cus * 256 * 256)
+    if (out >= kTile256 * dev.cus)
         return run_fp4<256, 256, 2, 4, 1>(a, workspace, dev, stream);
-    if (out >= (int64_t)dev.cus * 128 * 128)
-        return run_fp4<128, 128, 2, 2, 1>(a, workspace, dev, stream);
-    if (a.I <= 32 && a.J >= 64 * dev.cus)
-        return run_fp4<32, 128, 1, 4, 1>(a, workspace, dev, stream);
-    if (a.I <= 64 && a.J >= 64 * dev.cus)
+    if (a.I <= 32) return run_fp4<32, 128, 1, 4, 1>(a, workspace, dev, stream);
+    if (a.I <= 64 && a.J >= kWideRows * dev.cus)
         return run_fp4<64, 128, 1, 4, 1>(a, workspace, dev, stream);
-    if (a.I > 64 && a.C >= kLong) return run_fp4<128, 128, 2, 2, 2>(a, workspace, dev, stream);
-    if (a.I > 32) return run_fp4<64, 64, 2, 2, 4>(a, workspace, dev, stream);
-    return run_fp4<32, 128, 1, 4, 2>(a, workspace, dev, stream);
+    if (many_tiles(a, dev))
+        return run_fp4<128, 128, 2, 2, 1>(a, workspace, dev, stream);
+    if (out >= kTile64 * dev.cus)
+        return run_fp4<128, 128, 2, 2, 2>(a, workspace, dev, stream);
+    return run_fp4<64, 64, 2, 2, 4>(a, workspace, dev, stream);
 }
 
 template <int LEFT, int RIGHT>
 hipError_t choose_tile(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                        hipStream_t stream) {
     const int64_t out = (int64_t)a.I * a.J;
-    if (out >= (int64_t)dev.cus * 256 * 256 / 2)
+    if (out >= kTile256 * dev.cus)
         return run_tile<256, 256, 2, 4, 1, LEFT, RIGHT>(a, workspace, dev, stream);
-    if (out >= (int64_t)dev.cus * 128 * 128)
+    if (many_tiles(a, dev))
         return run_tile<128, 128, 2, 2, 1, LEFT, RIGHT>(a, workspace, dev, stream);
-    if (a.I > 64 && a.C >= kLong)
+    if (out >= kTile64 * dev.cus || (a.I > 64 && a.C >= kLong))
         return run_tile<128, 128, 2, 2, 2, LEFT, RIGHT>(a, workspace, dev, stream);
     return run_tile<64, 64, 2, 2, 4, LEFT, RIGHT>(a, workspace, dev, stream);
 }
-
 
 template <int FMT, int DT>
 hipError_t run_quantize(const MxCastArgs &a, hipStream_t stream) {
