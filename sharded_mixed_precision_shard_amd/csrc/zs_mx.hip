@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize(MxCastArgs a) {
 #pragma unroll
     for (int u = 0; u < kCastUnroll; ++u) {
         const int64_t block = first + u * (kThreads / 4);
-        const int64_t row = a.nb < a.blocks ? block / a.nb : 0;
+        const int64_t row = a.nb < a.blocks ? (uint32_t)block / (uint32_t)a.nb : 0;
         const int64_t col = (block - row * a.nb) * kMxBlock + part * 8;
         load8<DT>(a.x, row * a.ld + col, block < a.blocks ? a.cols - col : 0, v[u]);
     }
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize(MxCastArgs a) {
 #pragma unroll
     for (int u = 0; u < kCastUnroll; ++u) {
         const int64_t block = first + u * (kThreads / 4);
-        const int64_t row = a.nb < a.blocks ? block / a.nb : 0;
+        const int64_t row = a.nb < a.blocks ? (uint32_t)block / (uint32_t)a.nb : 0;
         const int64_t col = (block - row * a.nb) * kMxBlock + part * 8;
         const float s = scale_of(scale[u]);
         f32x2 w[4];
@@ -543,19 +543,14 @@ __device__ __forceinline__ void tile_of(int64_t block, int tiles_i, int tiles_j,
 }
 
 // The wave groups of a workgroup, each with a part of c: all but the first leave their sums
-// in LDS, a tile of them each in a and b (what fits a, and the rest in b), and the first
-// adds them in order.  True for the first.
-template <int KG, int FJ, int FI>
-__device__ __forceinline__ bool join_groups(f32x16 (&acc)[FJ][FI], char *a, char *b, int a_bytes,
-                                            int tile_bytes, int group, int wave, int lane) {
+// in LDS, wave by wave at scratch(group, wave), and the first adds them in order.  True for
+// the first; the others end, and the barriers behind this wait for its waves alone.
+template <int KG, int FJ, int FI, class S>
+__device__ __forceinline__ bool join_groups(f32x16 (&acc)[FJ][FI], const S &scratch, int group,
+                                            int wave, int lane) {
     if constexpr (KG == 1) return true;
-    const int in_a = a_bytes / tile_bytes;
-    auto at = [&](int g) {
-        char *p = g - 1 < in_a ? a + (g - 1) * tile_bytes : b + (g - 1 - in_a) * tile_bytes;
-        return (f32x4 *)(p + wave * (FJ * FI * 4096)) + lane;
-    };
     if (group > 0) {
-        f32x4 *to = at(group);
+        f32x4 *to = (f32x4 *)scratch(group, wave) + lane;
 #pragma unroll
         for (int j = 0; j < FJ; ++j)
 #pragma unroll
@@ -570,7 +565,7 @@ __device__ __forceinline__ bool join_groups(f32x16 (&acc)[FJ][FI], char *a, char
     if (group > 0) return false;
 #pragma unroll
     for (int g = 1; g < KG; ++g) {
-        const f32x4 *from = at(g);
+        const f32x4 *from = (const f32x4 *)scratch(g, wave) + lane;
 #pragma unroll
         for (int j = 0; j < FJ; ++j)
 #pragma unroll
@@ -582,17 +577,19 @@ __device__ __forceinline__ bool join_groups(f32x16 (&acc)[FJ][FI], char *a, char
                     for (int e = 0; e < 4; ++e) acc[j][i][4 * r + e] += v[e];
                 }
     }
-    __syncthreads();  // the waves of the first group, for a and b to be written again
     return true;
 }
 
+// Bytes of LDS that a wave's scratch holds: its sums, or 4 KB to turn them in.
+constexpr int scratch_bytes(int groups, int frags) { return groups > 1 ? frags * 4096 : 4096; }
+
 // The end of a tile: its sums go out, or to the workspace, where another split finds them.
-// `stage` is 4 KB of LDS per wave that nothing reads any more.
+// `mine` is 4 KB of LDS of the wave's own.
 template <int BI, int BJ, int WI, int WJ>
 __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
                                             f32x16 (&acc)[BJ / WJ / 32][BI / WI / 32],
                                             int tile, int split, int i0, int j0, int wi, int wj,
-                                            int wave, int lane, uint32_t *shared, char *stage) {
+                                            int wave, int lane, uint32_t *shared, char *mine) {
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     // Splits are joined two by two: of splits [s, s + n) and [s + n, s + 2 n) the one that is
     // done first leaves its sums and ends, the other adds them to its own and goes on with
@@ -605,14 +602,14 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
         if (other >= a.splits) continue;
         uint32_t *counter = a.counters + (int64_t)tile * a.splits + s + n;
         if (!arrived(counter, shared)) {
-            const uint32_t mine = (slots + (uint32_t)(split & ~(n - 1))) * (BI * BJ) + here;
+            const uint32_t to = (slots + (uint32_t)(split & ~(n - 1))) * (BI * BJ) + here;
 #pragma unroll
             for (int j = 0; j < FJ; ++j)
 #pragma unroll
                 for (int i = 0; i < FI; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        put_part(a.parts, mine + ((j * FI + i) * 4 + r) * 256,
+                        put_part(a.parts, to + ((j * FI + i) * 4 + r) * 256,
                                  f32x4{acc[j][i][4 * r], acc[j][i][4 * r + 1],
                                        acc[j][i][4 * r + 2], acc[j][i][4 * r + 3]});
             if (!last_split(counter, 2, shared)) return;
@@ -634,7 +631,6 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
     }
     // A lane holds four neighbours of one row of out.  Through LDS a wave's 32 rows leave in
     // stretches of 64 or 128 bytes (bf16; 128 in fp32), 16 bytes a lane.
-    char *mine = stage + wave * 4096;
     const int i = lane % 32, half = lane / 32, row = lane / 8, chunk = lane % 8;
     constexpr int PAIR = FJ % 2 == 0 ? 2 : 1;  // fragments side by side in a row of bf16
 #pragma unroll
@@ -800,9 +796,12 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile(MxProductArgs a)
 
     __shared__ uint32_t shared;
     __syncthreads();
-    if (join_groups<KG>(acc, all[0], all[0], (int)sizeof(all), BI * BJ * 4, group, wave, lane))
+    constexpr int EACH = 2 * (P_BYTES + Q_BYTES) / (WI * WJ);
+    static_assert(EACH >= scratch_bytes(KG, FI * FJ), "scratch");
+    auto scratch = [&](int g, int w) { return all[g] + w * EACH; };
+    if (join_groups<KG>(acc, scratch, group, wave, lane))
         finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, &shared,
-                                    all[0]);
+                                    scratch(0, wave));
 }
 
 // ---------------------------------------------- products of two fp4 operands
@@ -947,7 +946,7 @@ mx_tile_fp4(MxProductArgs a) {
         // instruction
 #define ZS_MX_QUARTER(S)                                                                       \
     {                                                                                          \
-        const int at = ((4 * h + S) ^ (r >> 1 & 7)) << 4;                                           \
+        const int at = ((4 * h + S) ^ (r >> 1 & 7)) << 4;                                      \
         i32x8 pf[FI], qf[FJ];                                                                  \
         _Pragma("unroll") for (int i = 0; i < FI; ++i) pf[i] =                                 \
             codes4(*(const u32x4 *)(p + i * 4096 + at));                                       \
@@ -986,9 +985,14 @@ mx_tile_fp4(MxProductArgs a) {
         put_scales(scales0, s);
     }
     stage_ready<0>();
-    if (join_groups<KG>(acc, all0[0], all1[0], (int)sizeof(all0), BI * BJ * 4, group, wave, lane))
+    constexpr int HALF = WI * WJ / 2, SCRATCH = (P_BYTES + Q_BYTES) / HALF;
+    static_assert(SCRATCH >= scratch_bytes(KG, FI * FJ), "scratch");
+    auto scratch = [&](int g, int w) {
+        return (w < HALF ? all0[g] : all1[g]) + w % HALF * SCRATCH;
+    };
+    if (join_groups<KG>(acc, scratch, group, wave, lane))
         finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
-                                    (uint32_t *)all_scales0, all0[0]);
+                                    (uint32_t *)all_scales0, scratch(0, wave));
 }
 
 // ------------------------------------- bf16 against blocks, rows in full chunks
@@ -1027,7 +1031,8 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductAr
     const int r = lane % 32, h = lane / 32;
 
     const uint32_t row_bytes = (uint32_t)a.ldp * 2u;
-    const auto p_buf = buffer_of(a.p + (int64_t)i0 * a.ldp, (uint32_t)min(a.I - i0, BI) * row_bytes);
+    const auto p_buf =
+        buffer_of(a.p + (int64_t)i0 * a.ldp, (uint32_t)min(a.I - i0, BI) * row_bytes);
     const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row >> 1 & 7);
     const uint32_t p_off = (uint32_t)row * row_bytes + (uint32_t)chunk * 16u;
     const uint8_t *codes[FJ];
@@ -1173,9 +1178,19 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductAr
     }
 #undef ZS_MX_STEP
     stage_ready<0>();
-    if (join_groups<KG>(acc, all0[0], all1[0], (int)sizeof(all0), BI * BJ * 4, group, wave, lane))
-        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
-                                    (uint32_t *)all3, all0[0]);
+    __shared__ uint32_t shared;
+    constexpr int QUARTER = WI * WJ / 4, SCRATCH = BI * 128 / QUARTER;
+    static_assert(SCRATCH >= scratch_bytes(KG, FI * FJ), "scratch");
+    auto scratch = [&](int g, int w) {
+        char *p = w / QUARTER == 0   ? all0[g]
+                  : w / QUARTER == 1 ? all1[g]
+                  : w / QUARTER == 2 ? all2[g]
+                                     : all3[g];
+        return p + w % QUARTER * SCRATCH;
+    };
+    if (join_groups<KG>(acc, scratch, group, wave, lane))
+        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, &shared,
+                                    scratch(0, wave));
 }
 
 // dx = dy w and dw = dy^T x: the stored operand's rows run along the output, so a fragment
@@ -1238,7 +1253,8 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
                 dma16(buf, lds + (k * NT + wave * kWave) * 16,
                       p_off + (uint32_t)(k * (NT / (BI / 8))) * p_row);
         } else {
-            const auto buf = buffer_of((const char *)a.p + p_at, (uint32_t)min(a.I - i0, BI) * p_row);
+            const auto buf =
+                buffer_of((const char *)a.p + p_at, (uint32_t)min(a.I - i0, BI) * p_row);
             // whole chunks only: the rest of a row is a step of its own
             const uint32_t off = c0 + chunk * 8 + 8 <= a.C ? p_off + (uint32_t)c0 * 2u : kNowhere;
 #pragma unroll
@@ -1352,10 +1368,19 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
         put_block(q0, b0);
     }
     stage_ready<0>();
-    if (join_groups<KG>(acc, all_p0[0], all_p1[0], (int)sizeof(all_p0), BI * BJ * 4, group, wave,
-                        lane))
-        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane,
-                                    (uint32_t *)all_q0, all_p0[0]);
+    __shared__ uint32_t shared;
+    constexpr int QUARTER = WI * WJ / 4, SCRATCH = (BI < BJ ? BI : BJ) * 128 / QUARTER;
+    static_assert(SCRATCH >= scratch_bytes(KG, FI * FJ), "scratch");
+    auto scratch = [&](int g, int w) {
+        char *p = w / QUARTER == 0   ? all_p0[g]
+                  : w / QUARTER == 1 ? all_p1[g]
+                  : w / QUARTER == 2 ? all_q0[g]
+                                     : all_q1[g];
+        return p + w % QUARTER * SCRATCH;
+    };
+    if (join_groups<KG>(acc, scratch, group, wave, lane))
+        finish_tile<BI, BJ, WI, WJ>(a, acc, tile, split, i0, j0, wi, wj, wave, lane, &shared,
+                                    scratch(0, wave));
 }
 
 // ------------------------------------------------------- products of few rows
