@@ -27,6 +27,21 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 // Vectors at any address that suits their elements.
 struct __attribute__((packed, aligned(2))) Any16 { u32x4 v; };
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+// Ordinary, or streaming: what is read or written once and does not fit the caches.
+template <bool NT>
+__device__ __forceinline__ u32x4 get16(const void *p) {
+    if constexpr (NT) return __builtin_nontemporal_load((const u32x4_any *)p);
+    return ((const Any16 *)p)->v;
+}
+template <bool NT>
+__device__ __forceinline__ void set16(void *p, u32x4 v) {
+    if constexpr (NT)
+        __builtin_nontemporal_store(v, (u32x4_any *)p);
+    else
+        ((Any16 *)p)->v = v;
+}
 
 __device__ __forceinline__ float scale_of(uint32_t b) { return __uint_as_float(b << 23); }
 
@@ -55,16 +70,18 @@ __device__ __forceinline__ i32x8 codes4(u32x4 v) {
 
 // Four lanes take a block, 8 elements each; a workgroup takes kCastUnroll times
 // 64 blocks.  Bound by memory: bf16 to fp8 moves 3.03 bytes per element, to fp4
-// 2.53, against about 3 vector instructions per element.
+// 2.53, against about 3 vector instructions per element.  6.7e7 bf16 elements to fp8 33 us
+// (6.1 TB/s), 8.1e8 to fp4 and back 651 us (6.3 TB/s).  Four blocks a thread: two take 34 and
+// 666, one 36 and 744.
 constexpr int kCastUnroll = 4;
 constexpr int kCastBlocks = kCastUnroll * kThreads / 4;
 
-template <int DT>
+template <int DT, bool NT>
 __device__ __forceinline__ void load8(const void *x, int64_t at, int64_t left, float v[8]) {
     if constexpr (DT == ZS_DTYPE_FP32) {
         const float *p = (const float *)x + at;
         if (left >= 8) {
-            const u32x4 a = ((const Any16 *)p)->v, b = ((const Any16 *)(p + 4))->v;
+            const u32x4 a = get16<NT>(p), b = get16<NT>(p + 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 v[e] = __uint_as_float(a[e]);
@@ -78,7 +95,7 @@ __device__ __forceinline__ void load8(const void *x, int64_t at, int64_t left, f
         const uint16_t *p = (const uint16_t *)x + at;
         u32x4 a = {0, 0, 0, 0};
         if (left >= 8) {
-            a = ((const Any16 *)p)->v;
+            a = get16<NT>(p);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -103,7 +120,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
     return m > b ? m : b;
 }
 
-template <int FMT, int DT>
+template <int FMT, int DT, int STREAM>
 __global__ __launch_bounds__(kThreads) void mx_quantize(MxCastArgs a) {
     const int part = threadIdx.x % 4;
     const int64_t first = (int64_t)blockIdx.x * kCastBlocks + threadIdx.x / 4;
@@ -113,7 +130,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize(MxCastArgs a) {
         const int64_t block = first + u * (kThreads / 4);
         const int64_t row = a.nb < a.blocks ? (uint32_t)block / (uint32_t)a.nb : 0;
         const int64_t col = (block - row * a.nb) * kMxBlock + part * 8;
-        load8<DT>(a.x, row * a.ld + col, block < a.blocks ? a.cols - col : 0, v[u]);
+        load8<DT, (STREAM > 0)>(a.x, row * a.ld + col, block < a.blocks ? a.cols - col : 0, v[u]);
     }
 #pragma unroll
     for (int u = 0; u < kCastUnroll; ++u) {
@@ -145,30 +162,39 @@ __global__ __launch_bounds__(kThreads) void mx_quantize(MxCastArgs a) {
                 w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[2], q[3], 1.0f, 1);
                 w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[4], q[5], 1.0f, 2);
                 w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, q[6], q[7], 1.0f, 3);
-                ((uint32_t *)a.codes)[block * 4 + part] = w;
+                uint32_t *to = (uint32_t *)a.codes + block * 4 + part;
+                if constexpr (STREAM > 1)
+                    __builtin_nontemporal_store(w, to);
+                else
+                    *to = w;
             } else {
                 s16x2 lo = {0, 0}, hi = {0, 0};
                 lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, q[0], q[1], 1.0f, false);
                 lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, q[2], q[3], 1.0f, true);
                 hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, q[4], q[5], 1.0f, false);
                 hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, q[6], q[7], 1.0f, true);
-                ((uint2 *)a.codes)[block * 4 + part] =
-                    uint2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+                uint64_t *to = (uint64_t *)a.codes + block * 4 + part;
+                const uint64_t w = (uint64_t)__builtin_bit_cast(uint32_t, hi) << 32 |
+                                   __builtin_bit_cast(uint32_t, lo);
+                if constexpr (STREAM > 1)
+                    __builtin_nontemporal_store(w, to);
+                else
+                    *to = w;
             }
             if (part == 0) a.scales[block] = finite ? (uint8_t)b : 255;
         }
     }
 }
 
-template <int DT>
+template <int DT, bool NT>
 __device__ __forceinline__ void store8(void *x, int64_t at, int64_t left, const float v[8]) {
     if constexpr (DT == ZS_DTYPE_FP32) {
         float *p = (float *)x + at;
         if (left >= 8) {
-            ((Any16 *)p)->v = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                    __float_as_uint(v[2]), __float_as_uint(v[3])};
-            ((Any16 *)(p + 4))->v = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                          __float_as_uint(v[6]), __float_as_uint(v[7])};
+            set16<NT>(p, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]),
+                               __float_as_uint(v[2]), __float_as_uint(v[3])});
+            set16<NT>(p + 4, u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]),
+                                   __float_as_uint(v[6]), __float_as_uint(v[7])});
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -185,8 +211,8 @@ __device__ __forceinline__ void store8(void *x, int64_t at, int64_t left, const 
                 h[e] = __builtin_bit_cast(uint16_t, (_Float16)v[e]);
         }
         if (left >= 8) {
-            ((Any16 *)p)->v = u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
-                                    h[6] | h[7] << 16};
+            set16<NT>(p, u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                               h[6] | h[7] << 16});
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -195,7 +221,7 @@ __device__ __forceinline__ void store8(void *x, int64_t at, int64_t left, const 
     }
 }
 
-template <int FMT, int DT>
+template <int FMT, int DT, bool NT>
 __global__ __launch_bounds__(kThreads) void mx_dequantize(MxCastArgs a) {
     const int part = threadIdx.x % 4;
     const int64_t first = (int64_t)blockIdx.x * kCastBlocks + threadIdx.x / 4;
@@ -235,7 +261,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize(MxCastArgs a) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = w[e / 2][e % 2];
-        if (block < a.blocks) store8<DT>(a.x, row * a.ld + col, a.cols - col, v);
+        if (block < a.blocks) store8<DT, NT>(a.x, row * a.ld + col, a.cols - col, v);
     }
 }
 
@@ -1820,17 +1846,35 @@ hipError_t choose_tile(const MxProductArgs &a, void *workspace, const MxDevice &
     return run_tile<64, 64, 2, 2, 4, LEFT, RIGHT>(a, workspace, dev, stream);
 }
 
+// Matrices from the size of the L2 caches on are streamed: 6.7e7 bf16 elements to fp8 33 us
+// against 37, and read back 30 and 40; 8.4e6 elements 9.9 either way.  The codes are, too, where
+// the last-level cache cannot hold both: to fp4 and back 8.1e8 bf16 elements 651 and 678 us,
+// 6.7e7 fp32 elements to fp8 and back 138 and 171, but 6.7e7 bf16 elements 69 and 63.
+constexpr int64_t kStreamBytes = int64_t(1) << 25;
+constexpr int64_t kStreamBoth = int64_t(1) << 28;
+
+constexpr int64_t dtype_bytes(int dtype) { return dtype == ZS_DTYPE_FP32 ? 4 : 2; }
+
 template <int FMT, int DT>
 hipError_t run_quantize(const MxCastArgs &a, hipStream_t stream) {
-    const int64_t groups = (a.blocks + kCastBlocks - 1) / kCastBlocks;
-    mx_quantize<FMT, DT><<<dim3((uint32_t)groups), dim3(kThreads), 0, stream>>>(a);
+    const dim3 grid((uint32_t)((a.blocks + kCastBlocks - 1) / kCastBlocks));
+    const int64_t bytes = a.blocks * kMxBlock * dtype_bytes(DT);
+    if (bytes + a.blocks * mx_block_bytes(FMT) >= kStreamBoth)
+        mx_quantize<FMT, DT, 2><<<grid, dim3(kThreads), 0, stream>>>(a);
+    else if (bytes >= kStreamBytes)
+        mx_quantize<FMT, DT, 1><<<grid, dim3(kThreads), 0, stream>>>(a);
+    else
+        mx_quantize<FMT, DT, 0><<<grid, dim3(kThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <int FMT, int DT>
 hipError_t run_dequantize(const MxCastArgs &a, hipStream_t stream) {
-    const int64_t groups = (a.blocks + kCastBlocks - 1) / kCastBlocks;
-    mx_dequantize<FMT, DT><<<dim3((uint32_t)groups), dim3(kThreads), 0, stream>>>(a);
+    const dim3 grid((uint32_t)((a.blocks + kCastBlocks - 1) / kCastBlocks));
+    if (a.blocks * kMxBlock * dtype_bytes(DT) >= kStreamBytes)
+        mx_dequantize<FMT, DT, true><<<grid, dim3(kThreads), 0, stream>>>(a);
+    else
+        mx_dequantize<FMT, DT, false><<<grid, dim3(kThreads), 0, stream>>>(a);
     return hipGetLastError();
 }
 
