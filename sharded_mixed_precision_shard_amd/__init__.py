@@ -1216,14 +1216,15 @@ _BYTES = -1
 _MATRIX_TYPE = {**ZS_DTYPE, "torch.int16": 0, "torch.uint16": 0, "torch.uint8": _BYTES}
 
 
-@functools.lru_cache(maxsize=None)
-def _type_code(dtype):
-    return _MATRIX_TYPE.get(str(dtype))
+class _TypeCodes(dict):
+    """Element type of a matrix (ZS_DTYPE), _BYTES, or None for any other, by dtype."""
+
+    def __missing__(self, dtype):
+        self[dtype] = _MATRIX_TYPE.get(str(dtype))
+        return self[dtype]
 
 
-def _matrix_type(x):
-    """Element type of a matrix (ZS_DTYPE), _BYTES, or None for any other."""
-    return _type_code(x.dtype)
+_type_codes = _TypeCodes()
 
 
 class Mx:
@@ -1236,7 +1237,7 @@ class Mx:
         code = ZS_MX_FORMAT.get(format)
         if code is None:
             raise ValueError("format: expected 'fp4' or 'fp8', got %r" % (format,))
-        if _matrix_type(codes) != _BYTES or _matrix_type(scales) != _BYTES:
+        if _type_codes[codes.dtype] != _BYTES or _type_codes[scales.dtype] != _BYTES:
             _check_type((codes,), ("torch.uint8",), "codes")
             _check_type((scales,), ("torch.uint8",), "scales")
         cols = int(cols)
@@ -1304,7 +1305,7 @@ def _matrix(x, name) -> ZsMatrix:
     if not getattr(x, "is_cuda", False):
         raise ValueError("%s must be a GPU tensor (got %s)" % (name, getattr(x, "device",
                                                                              type(x))))
-    dtype = _matrix_type(x)
+    dtype = _type_codes[x.dtype]
     if dtype is None or dtype == _BYTES:
         raise TypeError("%s: %s is not bfloat16, float16 or float32" % (name, x.dtype))
     shape, strides = x.shape, x.stride()
@@ -1339,17 +1340,20 @@ def _mx_ready(name, held, first, second=None, workspace=None):
     """Refuse buffers of several devices or of one that is not current, and a
     workspace that belongs to a graph; the workspace's address."""
     index = held.index
-    if first.get_device() != index if not isinstance(first, Mx) else first.index != index:
+    other = first.index if isinstance(first, Mx) else first.get_device()
+    if other != index or (second is not None and second.get_device() != index):
         raise ValueError("%s: buffers on different devices" % name)
-    if second is not None and second.get_device() != index:
-        raise ValueError("%s: buffers on different devices" % name)
-    _on_device(index)
+    if _current_device is None or _current_device() != index:
+        _on_device(index)
     if workspace is None:
         return None
     if getattr(workspace, "made_in_capture", False):
         _graph_only(name)
-    if not isinstance(workspace, int) and workspace.get_device() not in (index, -1):
-        raise ValueError("%s: buffers on different devices" % name)
+    if getattr(workspace, "is_cuda", False) and workspace.is_contiguous() and \
+            workspace.numel() * workspace.element_size() >= ZS_MX_WORKSPACE_BYTES:
+        if workspace.get_device() != index:
+            raise ValueError("%s: buffers on different devices" % name)
+        return workspace.data_ptr()
     return _dev(workspace, ZS_MX_WORKSPACE_BYTES, "workspace")
 
 
@@ -1364,7 +1368,7 @@ def zs_mx_quantize(x, out, stream=None, check=True) -> int:
     of its size."""
     m, ref = _matrix(x, "x"), _held(out, "out")
     _mx_ready("zs_mx_quantize", out, x)
-    rc = load_library().zs_mx_quantize(ctypes.byref(m), ref, _stream_handle(stream))
+    rc = (_lib or load_library()).zs_mx_quantize(ctypes.byref(m), ref, _stream_handle(stream))
     return _mx_done(rc, "zs_mx_quantize", check)
 
 
@@ -1372,7 +1376,7 @@ def zs_mx_dequantize(x, out, stream=None, check=True) -> int:
     """Write the values of an Mx into a matrix of its size (bf16, fp16 or fp32)."""
     ref, m = _held(x, "x"), _matrix(out, "out")
     _mx_ready("zs_mx_dequantize", x, out)
-    rc = load_library().zs_mx_dequantize(ref, ctypes.byref(m), _stream_handle(stream))
+    rc = (_lib or load_library()).zs_mx_dequantize(ref, ctypes.byref(m), _stream_handle(stream))
     return _mx_done(rc, "zs_mx_dequantize", check)
 
 
@@ -1382,7 +1386,7 @@ def zs_mx_linear(x, w, y, stream=None, workspace=None, check=True) -> int:
     sum over more of the device."""
     ref, mx, my = _held(w, "w"), _matrix(x, "x"), _matrix(y, "y")
     space = _mx_ready("zs_mx_linear", w, x, y, workspace)
-    rc = load_library().zs_mx_linear(ctypes.byref(mx), ref, ctypes.byref(my), space,
+    rc = (_lib or load_library()).zs_mx_linear(ctypes.byref(mx), ref, ctypes.byref(my), space,
                                      _stream_handle(stream))
     return _mx_done(rc, "zs_mx_linear", check)
 
@@ -1391,7 +1395,8 @@ def zs_mx_product(x, w, y, stream=None, workspace=None, check=True) -> int:
     """zs_mx_linear of an x that is an Mx itself."""
     ref, refx, my = _held(w, "w"), _held(x, "x"), _matrix(y, "y")
     space = _mx_ready("zs_mx_product", w, x, y, workspace)
-    rc = load_library().zs_mx_product(refx, ref, ctypes.byref(my), space, _stream_handle(stream))
+    rc = (_lib or load_library()).zs_mx_product(refx, ref, ctypes.byref(my), space,
+                                                _stream_handle(stream))
     return _mx_done(rc, "zs_mx_product", check)
 
 
@@ -1399,7 +1404,7 @@ def zs_mx_linear_dgrad(dy, w, dx, stream=None, workspace=None, check=True) -> in
     """dx [M, K] = dy [M, N] w for a bf16 dy and an Mx w [N, K]; dx is bf16 or fp32."""
     ref, my, mx = _held(w, "w"), _matrix(dy, "dy"), _matrix(dx, "dx")
     space = _mx_ready("zs_mx_linear_dgrad", w, dy, dx, workspace)
-    rc = load_library().zs_mx_linear_dgrad(ctypes.byref(my), ref, ctypes.byref(mx), space,
+    rc = (_lib or load_library()).zs_mx_linear_dgrad(ctypes.byref(my), ref, ctypes.byref(mx), space,
                                            _stream_handle(stream))
     return _mx_done(rc, "zs_mx_linear_dgrad", check)
 
@@ -1409,6 +1414,6 @@ def zs_mx_linear_wgrad(dy, x, dw, add=False, stream=None, workspace=None, check=
     Mx; dw is bf16 (a partial of the step) or fp32, where ``add`` adds to it."""
     ref, my, mw = _held(x, "x"), _matrix(dy, "dy"), _matrix(dw, "dw")
     space = _mx_ready("zs_mx_linear_wgrad", x, dy, dw, workspace)
-    rc = load_library().zs_mx_linear_wgrad(ctypes.byref(my), ref, ctypes.byref(mw),
+    rc = (_lib or load_library()).zs_mx_linear_wgrad(ctypes.byref(my), ref, ctypes.byref(mw),
                                            1 if add else 0, space, _stream_handle(stream))
     return _mx_done(rc, "zs_mx_linear_wgrad", check)

@@ -11,6 +11,7 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+import tempfile
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
@@ -86,10 +87,23 @@ def build(verbose: bool = False) -> str:
     """Compile libzs.so, libzs_host.so and libzs_ceiling.so (always
     recompiles).  Returns the device library path."""
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, "-I", INCLUDE_DIR, "-o", tmp, *SRCS]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as objects:
+        # the sources side by side: they are independent, and one after the other takes minutes
+        jobs, objs = [], []
+        for src in SRCS:
+            objs.append(os.path.join(objects, os.path.basename(src) + ".o"))
+            cmd = [hipcc(), *flags, "-I", INCLUDE_DIR, "-c", "-o", objs[-1], src]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            jobs.append((cmd, subprocess.Popen(cmd)))
+        failed = [cmd for cmd, job in jobs if job.wait() != 0]
+        if failed:
+            raise subprocess.CalledProcessError(1, failed[0])
+        cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-o", tmp, *objs]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     build_host(verbose)
     build_ceiling(verbose)

@@ -5,11 +5,15 @@ weights' gradients made from those as the partial that norm and clipped step tak
 Every stage is held against a plain implementation in 64 bits on the inputs that the stage
 had.  Tolerances: codes, scales and the step are exact; an fp32 sum of C exact products is
 within C 2^-23 sum|p|, a bf16 output of it half a step, 2^-8, more."""
+import os
+import re
+
 import numpy as np
 import pytest
 
 import sharded_mixed_precision_shard_amd as zs
 from tests import _mx_reference as ref
+from tests.conftest import ROOT
 from tests.test_gpu_norm import gpu  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -183,3 +187,39 @@ def test_buffers_of_a_device_that_is_not_current_are_refused(gpu, monkeypatch):
     monkeypatch.setattr(zs, "_current_device", lambda: 7)
     with pytest.raises(ValueError, match="current device"):
         zs.zs_mx_quantize(x, held)
+
+
+def test_the_readme_recipe(gpu, monkeypatch):
+    """The recipe of README.md as it is printed, on one of two ranks whose shards are alike (the
+    all-gather, a stand-in, finds the same blocks on both), on a stream of its own."""
+    torch = gpu
+    text = open(os.path.join(ROOT, "README.md")).read()
+    recipe, = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "zs_mx_linear" in b]
+    stream = torch.cuda.Stream()
+
+    def all_gather_into_tensor(out, mine):
+        assert torch.cuda.current_stream() == stream
+        out.copy_(mine.expand_as(out))
+
+    monkeypatch.setattr(torch.distributed, "all_gather_into_tensor", all_gather_into_tensor)
+    gen = torch.Generator().manual_seed(3)
+    n, ranks, tokens, inputs, outputs, start = 6400, 2, 50, 96, 70, 3200
+    param = torch.randn(n, generator=gen).to(torch.bfloat16).cuda()
+    x = torch.randn(tokens, inputs, generator=gen).to(torch.bfloat16).cuda()
+    dy = torch.randn(tokens, outputs, generator=gen).to(torch.bfloat16).cuda()
+    partial = torch.zeros(n * ranks, dtype=torch.bfloat16, device="cuda")
+    names = dict(zs=zs, torch=torch, device="cuda", stream=stream, n=n, ranks=ranks, param=param,
+                 tokens=tokens, inputs=inputs, outputs=outputs, start=start, x=x, dy=dy,
+                 y=torch.empty(tokens, outputs, dtype=torch.bfloat16, device="cuda"),
+                 dx=torch.empty(tokens, inputs, dtype=torch.bfloat16, device="cuda"),
+                 dw=partial[start:start + outputs * inputs].view(outputs, inputs))
+    torch.cuda.synchronize()
+    exec(recipe, names)
+    torch.cuda.synchronize()
+    held = ref.decode(*ref.encode(double(param)[None], "fp4"), "fp4", n)[0]
+    w = np.tile(held, ranks)[start:start + outputs * inputs].reshape(outputs, inputs)
+    kept = ref.decode(*ref.encode(double(x), "fp8"), "fp8", inputs)
+    near(names["y"], double(x), w.T)
+    near(names["dx"], double(dy), w)
+    near(names["dw"], double(dy).T, kept)
+    assert not partial[:start].any() and not partial[start + outputs * inputs:].any()
