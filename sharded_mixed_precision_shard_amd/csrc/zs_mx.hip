@@ -726,6 +726,11 @@ __device__ __forceinline__ int group_steps(const MxProductArgs &a, int depth, in
 // A workgroup makes a BI x BJ tile of out (of one split of c, in KG wave groups).  The matrix
 // instruction takes Q's rows as its rows and P's as its columns: a lane then
 // holds four neighbouring j's of one i, and stores them together.
+//
+// This one takes any strides and depths: both operands go through registers, a step ahead, with
+// loads of 16 bytes at addresses of 2.  Bound by what those registers leave to be in flight:
+// 4096^3 132 us on odd rows (1.04 PFLOP/s; 109 in the kernels below), 118 for fp8 by fp4, which
+// has no other.
 template <int BI, int BJ, int WI, int WJ, int KG, int LEFT, int RIGHT>
 __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
@@ -873,9 +878,14 @@ struct Scales8 {
 // Both operands' codes go into the scaled matrix instruction as they are: 64 products
 // of a row and a column per instruction, at four times the rate of bf16.  A lane holds
 // a block of 32, so its scale is one byte, taken from a word of four by number.
+//
+// 8192 x 28672 of depth 8192 1.04 ms (3.7 PFLOP/s, through bf16 instructions 4.5 ms), 4096^3 47
+// us.  The matrix pipe is busy 48 % of the time: of the 1.04 ms the transfers take 0.16, the
+// scales' way through LDS 0.07, the output 0.07, and each stage ends with both waves of a SIMD
+// at its barrier.  Two waves of 128 x 64 per SIMD, since one of 128 x 128 was given copies of all
+// its sums every turn.
 template <int BI, int BJ, int WI, int WJ, int KG>
-__global__ __launch_bounds__(WI *WJ *KG *kWave, BI *BJ >= WI * WJ * 16384 ? 1 : 2) void
-mx_tile_fp4(MxProductArgs a) {
+__global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     constexpr int P_BYTES = BI * 128, Q_BYTES = BJ * 128;
@@ -1031,6 +1041,11 @@ constexpr int64_t kReach = int64_t(1) << 31;
 // loads the block that it multiplies straight into registers, three steps ahead, and
 // widens it there, so LDS carries only x.  Half a wave (32 rows of w) takes one of a
 // step's two blocks, and the four instructions of a step its four words.
+//
+// 8192 x 11008 of depth 4096 0.60 ms (1.23 PFLOP/s; codes widened on their way into LDS 0.97),
+// the matrix pipe busy 73 % of the time and LDS 20 %, at a clock that the load holds at 1.6 GHz.
+// Fragments read an instruction ahead by hand (0.66), raised wave priority around the matrix
+// instructions (0.62) and staggered steps (0.65) were no faster.
 template <int BI, int BJ, int WI, int WJ, int KG, bool F8>
 __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
@@ -1224,6 +1239,11 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductAr
 // LDS column-major, where the transposing reads take it from; dy goes there by DMA.  Both
 // operands' addresses move with c, so a 32-bit offset never passes a step; rows past the
 // last read as zeros.
+//
+// dgrad, 8192 x 4096 of depth 11008 0.58 ms (1.27 PFLOP/s, the matrix pipe busy 66 % of the time,
+// LDS 42 %); wgrad, 4096 x 11008 of depth 8192 in fp8 0.68 (1.08; 55-59 % and 37 %).  LDS carries
+// both operands and their writes here, and is what bounds the small tiles: 64 x 64 takes three
+// times as long per product.
 template <int BI, int BJ, int WI, int WJ, int KG, bool PC, bool F8>
 __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
@@ -1415,7 +1435,8 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductAr
 // 16 blocks (kTurn) at a time, the waves of a workgroup in turn along the row.  Of a turn
 // the lanes of quarter g load the blocks 4 u + g, u = 0 .. 3: 64 neighbouring bytes of a row
 // at a time.  The sums of the waves are joined in LDS, those of the workgroups that share
-// a strip in the workspace.
+// a strip in the workspace.  One row, N = 11008, K = 4096 9.0 us (24 MB, 2.6 TB/s, the caches
+// holding w); 8 rows of fp4, N = 28672, K = 8192 32 us (125 MB, 3.9 TB/s, from memory).
 constexpr int kTurn = 16;
 
 struct __attribute__((packed, aligned(1))) Bytes16 { u32x4 v; };

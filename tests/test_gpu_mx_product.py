@@ -429,3 +429,55 @@ def test_narrow_gradients(gpu, workspace, n, pad):
             _, out = case.out(torch.float32)
             case.call(out, space)
             case.check_equal(out)
+
+
+@pytest.mark.parametrize("op", ["linear", "product", "dgrad", "wgrad"])
+@pytest.mark.parametrize("pad", [0, 1])
+def test_offsets_past_32_bits(gpu, workspace, op, pad):
+    """Operands and outputs of more than 2^31 elements or 2^32 bytes: zeros but for a few rows
+    near the end, whose products arrive where they belong."""
+    torch = gpu
+    rows, n, k = 2_100_007, 72, 1056
+    rng = np.random.default_rng(4)
+    last = torch.tensor([rows - 70, rows - 2, rows - 1])
+    w, wv = held(torch, rng, n, k, "fp4", True)
+    if op in ("linear", "product"):
+        x, xv = plain(torch, rng, 3, k, True, 0, 0)
+        y = torch.full((rows, n), 7.0, device="cuda")
+        if op == "linear":
+            full = torch.zeros(rows, k + pad, dtype=torch.bfloat16, device="cuda")[:, :k]
+            full[last.cuda()] = x
+            zs.zs_mx_linear(full, w, y, torch.cuda.current_stream(), workspace)
+            want = xv @ wv.T
+        else:
+            full, few = zs.Mx.empty(rows, k, "fp8"), zs.Mx.empty(3, k, "fp8")
+            zs.zs_mx_quantize(x, few, torch.cuda.current_stream())
+            full.codes.zero_()
+            full.scales.fill_(127)
+            full.codes[last.cuda()] = few.codes
+            full.scales[last.cuda()] = few.scales
+            zs.zs_mx_product(full, w, y, torch.cuda.current_stream(), workspace)
+            want = ref.decode(few.codes.cpu().numpy(), few.scales.cpu().numpy(), "fp8", k) @ wv.T
+        assert np.array_equal(y[last.cuda()].cpu().numpy(), want.astype(np.float32))
+        assert int((y != 0).any(1).sum()) == 3
+    elif op == "dgrad":
+        dy, dv = plain(torch, rng, 3, n, True, 0, 0)
+        full = torch.zeros(rows, n + 8 * pad + pad, dtype=torch.bfloat16, device="cuda")[:, :n]
+        full[last.cuda()] = dy
+        dx = torch.full((rows, k), 7.0, dtype=torch.bfloat16, device="cuda")
+        zs.zs_mx_linear_dgrad(full, w, dx, torch.cuda.current_stream(), workspace)
+        assert np.array_equal(dx[last.cuda()].float().cpu().numpy(), ref.bf16_round(dv @ wv))
+        assert int((dx != 0).any(1).sum()) == 3
+    else:
+        dy, dv = plain(torch, rng, 3, n, True, 0, 0)
+        few, fv = held(torch, rng, 3, k, "fp8", True)
+        full = torch.zeros(rows, n + pad, dtype=torch.bfloat16, device="cuda")[:, :n]
+        full[last.cuda()] = dy
+        x = zs.Mx.empty(rows, k, "fp8")
+        x.codes.fill_(0x38)                          # ones, against zeros of dy
+        x.scales.fill_(127)
+        x.codes[last.cuda()] = few.codes
+        x.scales[last.cuda()] = few.scales
+        dw = torch.empty(n, k, device="cuda")
+        zs.zs_mx_linear_wgrad(full, x, dw, False, torch.cuda.current_stream(), workspace)
+        assert np.array_equal(dw.cpu().numpy(), (dv.T @ fv).astype(np.float32))
