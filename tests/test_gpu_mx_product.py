@@ -481,3 +481,30 @@ def test_offsets_past_32_bits(gpu, workspace, op, pad):
         dw = torch.empty(n, k, device="cuda")
         zs.zs_mx_linear_wgrad(full, x, dw, False, torch.cuda.current_stream(), workspace)
         assert np.array_equal(dw.cpu().numpy(), (dv.T @ fv).astype(np.float32))
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("spread", [10, 60])
+def test_scales_far_apart(gpu, workspace, op, spread):
+    """Blocks whose powers of two differ by up to 2^120 in one sum: within the same bound."""
+    torch = gpu
+    size = {"wgrad": (500, 90, 100), "dgrad": (90, 500, 100)}.get(op, (90, 100, 500))
+    case = Case(torch, op, *size, "fp4", False, 8)
+    rng = np.random.default_rng(9)
+    for mx in (case.a, case.b):
+        if isinstance(mx, zs.Mx):
+            s = rng.integers(127 - spread, 128 + spread, tuple(mx.scales.shape)).astype(np.uint8)
+            mx.scales.copy_(torch.from_numpy(s))
+
+    def value(x):
+        return ref.decode(x.codes.cpu().numpy(), x.scales.cpu().numpy(), x.format, x.cols) \
+            if isinstance(x, zs.Mx) else x.double().cpu().numpy()
+
+    a, b = value(case.a), value(case.b)
+    a, b = (a.T if op == "wgrad" else a), (b if op in ("dgrad", "wgrad") else b.T)
+    case.want, case.sizes = a @ b, np.abs(a) @ np.abs(b)
+    for kind in (torch.float32, torch.bfloat16):
+        for space in (None, workspace):
+            _, out = case.out(kind)
+            case.call(out, space)
+            case.check_near(out)
