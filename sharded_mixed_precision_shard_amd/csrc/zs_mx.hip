@@ -1668,9 +1668,14 @@ __global__ __launch_bounds__(WAVES *kWave) void mx_few(MxProductArgs a) {
 }
 
 // Tiles of out and splits of c for a kernel of bi x bj tiles whose steps take `depth` c's
-// and whose splits are `groups` parts of whole turns of `turn` steps each.
-void plan(MxProductArgs *a, int bi, int bj, int groups, int depth, int turn, void *workspace,
-          const MxDevice &dev) {
+// and whose splits are `groups` parts of whole turns of `turn` steps each, `least` steps at
+// least for a part: below that the join costs more than the shorter part saves. Eight, but
+// four for the fp4 kernel, whose steps are deeper. Measured with eight and with four: fp4
+// product 64 x 4096 of depth 8192 19.8 and 14.4 us (depth 4096 10.7 both); linear 32 x 4096
+// of depth 4096 11.6 and 13.4; dgrad 64 x 4096 of depth 4096 18.7 and 21.4, though 128 x 768
+// of depth 2048 12.2 and 10.7.
+void plan(MxProductArgs *a, int bi, int bj, int groups, int depth, int turn, int least,
+          void *workspace, const MxDevice &dev) {
     a->tiles_i = (a->I + bi - 1) / bi;
     a->tiles_j = (a->J + bj - 1) / bj;
     const int64_t tiles = (int64_t)a->tiles_i * a->tiles_j;
@@ -1680,7 +1685,7 @@ void plan(MxProductArgs *a, int bi, int bj, int groups, int depth, int turn, voi
     const int64_t most = groups == 1 && bi * bj <= 64 * 128 ? 2 * dev.cus : dev.cus;
     if (workspace && tiles < most && most <= kMxCounters) {
         splits = most / tiles;
-        splits = splits < steps / (8 * groups) ? splits : steps / (8 * groups);
+        splits = splits < steps / (least * groups) ? splits : steps / (least * groups);
         const int64_t room = kMxPartBytes / (tiles * bi * bj * 4);
         splits = splits < room ? splits : room;
         splits = splits > 1 ? splits : 1;
@@ -1722,7 +1727,7 @@ dim3 grid_of(const MxProductArgs &a) {
 
 template <int BI, int BJ, int WI, int WJ, int KG, int LEFT, int RIGHT>
 hipError_t run_tile(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    plan(&a, BI, BJ, KG, kStep, 1, workspace, dev);
+    plan(&a, BI, BJ, KG, kStep, 1, 8, workspace, dev);
     mx_tile<BI, BJ, WI, WJ, KG, LEFT, RIGHT>
         <<<grid_of(a), dim3(WI * WJ * KG * kWave), 0, stream>>>(a);
     return hipGetLastError();
@@ -1730,7 +1735,7 @@ hipError_t run_tile(MxProductArgs a, void *workspace, const MxDevice &dev, hipSt
 
 template <int BI, int BJ, int WI, int WJ, int KG>
 hipError_t run_fp4(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    plan(&a, BI, BJ, KG, kStep4, 2, workspace, dev);
+    plan(&a, BI, BJ, KG, kStep4, 2, 4, workspace, dev);
     mx_tile_fp4<BI, BJ, WI, WJ, KG>
         <<<grid_of(a), dim3(WI * WJ * KG * kWave), 0, stream>>>(a);
     return hipGetLastError();
@@ -1738,7 +1743,7 @@ hipError_t run_fp4(MxProductArgs a, void *workspace, const MxDevice &dev, hipStr
 
 template <int BI, int BJ, int WI, int WJ, int KG, bool F8>
 hipError_t run_rows(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    plan(&a, BI, BJ, KG, kStep, 4, workspace, dev);
+    plan(&a, BI, BJ, KG, kStep, 4, 8, workspace, dev);
     mx_tile_rows<BI, BJ, WI, WJ, KG, F8>
         <<<grid_of(a), dim3(WI * WJ * KG * kWave), 0, stream>>>(a);
     return hipGetLastError();
@@ -1814,7 +1819,7 @@ hipError_t choose_rows(const MxProductArgs &a, void *workspace, const MxDevice &
 
 template <int BI, int BJ, int WI, int WJ, int KG, bool PC, bool F8>
 hipError_t run_cols(MxProductArgs a, void *workspace, const MxDevice &dev, hipStream_t stream) {
-    plan(&a, BI, BJ, KG, kStep, 2, workspace, dev);
+    plan(&a, BI, BJ, KG, kStep, 2, 8, workspace, dev);
     mx_tile_cols<BI, BJ, WI, WJ, KG, PC, F8>
         <<<grid_of(a), dim3(WI * WJ * KG * kWave), 0, stream>>>(a);
     return hipGetLastError();

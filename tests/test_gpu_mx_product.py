@@ -161,6 +161,7 @@ def test_normals(gpu, workspace, op, fmt):
 @pytest.mark.parametrize("op,size", [
     ("linear", (1, 100, 20000)), ("linear", (33, 64, 9000)), ("linear", (8, 4096, 1024)),
     ("product", (1, 100, 20000)), ("product", (70, 300, 8192)), ("product", (16, 4096, 2048)),
+    ("product", (65, 4096, 8190)), ("product", (70, 200, 2337)), ("product", (33, 500, 4609)),
     ("dgrad", (5, 20000, 70)), ("dgrad", (129, 9000, 130)), ("dgrad", (1, 512, 4096)),
     ("wgrad", (20000, 60, 70)), ("wgrad", (9001, 129, 257)), ("wgrad", (4096, 128, 1024))])
 @pytest.mark.parametrize("fmt", ["fp4", "fp8"])
