@@ -861,6 +861,13 @@ __device__ __forceinline__ void stage_ready() {
     asm volatile("" ::: "memory");
 }
 
+// Memory operations before this are issued before those behind it.  A wait for all but the N
+// newest operations is one for a transfer only as long as N others follow it.
+__device__ __forceinline__ void in_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // Eight scales of a row from `block` on, inside the row, shifted where they reach back: what
 // is past the row's end becomes 0 or 1, scales that stand for numbers.  No branch: in the
 // loops below one would cost registers that the sums need.
@@ -1179,14 +1186,18 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductAr
     // fp8 codes take twice the registers, and are loaded a step later
     constexpr int FAR = F8 ? 2 : 3;
     Codes q0, q1, q2, q3;
+    // the transfers first: the waits below count on what follows them
     fetch(lds0, 0);
-    q0 = fetch_codes(0);
     fetch(lds1, 1);
-    q1 = fetch_codes(1);
     fetch(lds2, 2);
+    in_order();
+    q0 = fetch_codes(0);
+    q1 = fetch_codes(1);
     if constexpr (FAR > 2) q2 = fetch_codes(2);
-    // Of each step EACH transfers to LDS are followed by FJ * W loads of codes; the
-    // transfers of two steps may be on their way while one is multiplied.
+    in_order();
+    // Each step issues EACH transfers to LDS and FJ * W loads of codes; those of two steps may
+    // be on their way while one is multiplied, and before the loop at least as many operations
+    // follow a step's transfers.
     constexpr int AHEAD = 2 * EACH + (F8 ? 1 : 2) * FJ * W;
 #define ZS_MX_STEP(T, HERE, Q, NEXT, QN)                                    \
     {                                                                       \
