@@ -1732,6 +1732,7 @@ constexpr int kLong = 8192;
 // N = 28672 53 and 68 (fp4 38 and 45), N = 16384 24 and 21 (16 and 15).
 constexpr int64_t kWideRows = 96;
 
+// Tiles of 256 x 256 are 2^21 at most, and where smaller ones are taken there are fewer.
 dim3 grid_of(const MxProductArgs &a) {
     return dim3((uint32_t)((int64_t)a.tiles_i * a.tiles_j * a.splits));
 }
@@ -1795,18 +1796,20 @@ hipError_t run_few(MxProductArgs a, void *workspace, const MxDevice &dev, hipStr
 // Strips of 64 columns read x a quarter as often as strips of 16, and leave a quarter of the
 // workgroups: bf16 x, K = 8192, N = 28672, 16 rows 42 us against 72, one row 36 and 38; K = 4096,
 // N = 11008, 16 rows 11.2 and 16.4, one row 10.3 and 9.2; N = 4096, 10.9 and 6.8.  An x in blocks
-// is short: strips of 16 are as fast or faster everywhere.
+// is short: strips of 16 are as fast or faster, up to the 2^23 of 512 threads each that are more
+// than a grid's dimension holds.
+constexpr int64_t kMostStrips = (int64_t(1) << 23) - 1;
+
 template <int LEFT, bool F8>
 hipError_t choose_few(const MxProductArgs &a, void *workspace, const MxDevice &dev,
                       hipStream_t stream) {
-    const int64_t wide = (a.I > 4 ? 32 : 64) * dev.cus;
-    if constexpr (LEFT == kLeftRows) {
+    const int64_t wide = LEFT != kLeftRows ? 16 * kMostStrips + 1 : (a.I > 4 ? 32 : 64) * dev.cus;
+    if constexpr (LEFT == kLeftRows)
         if (a.J >= wide && a.I <= 16)
             return run_few<LEFT, F8, 1, 4, 4>(a, workspace, dev, stream);
-        if (a.J >= wide && a.I <= 32)
-            return run_few<LEFT, F8, 2, 2, 4>(a, workspace, dev, stream);
-        if (a.J >= wide) return run_few<LEFT, F8, 4, 2, 4>(a, workspace, dev, stream);
-    }
+    if (a.J >= wide && a.I <= 32)
+        return run_few<LEFT, F8, 2, 2, 4>(a, workspace, dev, stream);
+    if (a.J >= wide) return run_few<LEFT, F8, 4, 2, 4>(a, workspace, dev, stream);
     if (a.I <= 16) return run_few<LEFT, F8, 1, 1, 8>(a, workspace, dev, stream);
     if (a.I <= 32) return run_few<LEFT, F8, 2, 1, 8>(a, workspace, dev, stream);
     return run_few<LEFT, F8, 4, 1, 8>(a, workspace, dev, stream);

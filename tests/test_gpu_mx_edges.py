@@ -244,3 +244,30 @@ def test_streamed_casts_equal_small_ones(gpu, fmt, kind):
                 assert torch.equal(whole.codes[row, first * each:last * each], part.codes[0])
                 assert torch.equal(whole.scales[row, first:last], part.scales[0])
                 assert torch.equal(back[row, a:b].view(torch.uint8), value.view(torch.uint8))
+
+
+@pytest.mark.parametrize("xfmt,wfmt,rows,n", [
+    ("fp4", "fp4", 1, 2 ** 27 + 5), ("fp8", "fp4", 17, 2 ** 27 + 21), ("fp4", "fp8", 2, 2 ** 28),
+    ("fp4", "fp4", 33, 2 ** 27), ("fp4", "fp4", 3, 2 ** 27 - 16)])
+def test_more_columns_than_a_grid_dimension_holds(gpu, xfmt, wfmt, rows, n):
+    """A few rows through as many rows of w as the library takes: strips of 16 of them with
+    512 threads each are 2^32 threads from 2^27 on.  Zeros but for rows near both ends and at
+    the border."""
+    torch = gpu
+    rng = np.random.default_rng(rows)
+    x, xv = held(torch, rng, rows, 32, xfmt, True)
+    at = {0, 15, 16, 2 ** 26 + 1, 2 ** 27 - 17, 2 ** 27 - 16, 2 ** 27 - 1, n - 2, n - 1}
+    at = sorted(i for i in at if i < n)
+    few, wv = held(torch, rng, len(at), 32, wfmt, True)
+    w = zs.Mx.empty(n, 32, wfmt)
+    w.codes.zero_()
+    w.scales.fill_(127)
+    where = torch.tensor(at, device="cuda")
+    w.codes[where] = few.codes
+    w.scales[where] = few.scales
+    y = torch.full((rows, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    zs.zs_mx_product(x, w, y, torch.cuda.current_stream())
+    want = ref.bf16_round(xv @ wv.T)
+    assert np.array_equal(y[:, where].float().cpu().numpy(), want)
+    y[:, where] = 0.0
+    assert not y.any()
