@@ -75,6 +75,12 @@ __device__ __forceinline__ i32x8 codes4(u32x4 v) {
 // 666, one 36 and 744.
 constexpr int kCastUnroll = 4;
 constexpr int kCastBlocks = kCastUnroll * kThreads / 4;
+// A grid's dimension holds fewer than 2^32 threads, and 2^32 - 1 blocks take as many: workgroups
+// are numbered along x in rows of 2^31 threads.
+constexpr int64_t kCastRow = (int64_t(1) << 31) / kThreads;
+__device__ __forceinline__ int64_t cast_block() {
+    return (blockIdx.y * kCastRow + blockIdx.x) * kCastBlocks + threadIdx.x / 4;
+}
 
 template <int DT, bool NT>
 __device__ __forceinline__ void load8(const void *x, int64_t at, int64_t left, float v[8]) {
@@ -123,7 +129,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
 template <int FMT, int DT, int STREAM>
 __global__ __launch_bounds__(kThreads) void mx_quantize(MxCastArgs a) {
     const int part = threadIdx.x % 4;
-    const int64_t first = (int64_t)blockIdx.x * kCastBlocks + threadIdx.x / 4;
+    const int64_t first = cast_block();
     float v[kCastUnroll][8];
 #pragma unroll
     for (int u = 0; u < kCastUnroll; ++u) {
@@ -224,7 +230,7 @@ __device__ __forceinline__ void store8(void *x, int64_t at, int64_t left, const 
 template <int FMT, int DT, bool NT>
 __global__ __launch_bounds__(kThreads) void mx_dequantize(MxCastArgs a) {
     const int part = threadIdx.x % 4;
-    const int64_t first = (int64_t)blockIdx.x * kCastBlocks + threadIdx.x / 4;
+    const int64_t first = cast_block();
     uint2 code[kCastUnroll];
     uint32_t scale[kCastUnroll];
 #pragma unroll
@@ -1895,9 +1901,15 @@ constexpr int64_t kStreamBoth = int64_t(1) << 28;
 
 constexpr int64_t dtype_bytes(int dtype) { return dtype == ZS_DTYPE_FP32 ? 4 : 2; }
 
+dim3 cast_grid(int64_t blocks) {
+    const int64_t groups = (blocks + kCastBlocks - 1) / kCastBlocks;
+    return dim3((uint32_t)(groups < kCastRow ? groups : kCastRow),
+                (uint32_t)((groups + kCastRow - 1) / kCastRow));
+}
+
 template <int FMT, int DT>
 hipError_t run_quantize(const MxCastArgs &a, hipStream_t stream) {
-    const dim3 grid((uint32_t)((a.blocks + kCastBlocks - 1) / kCastBlocks));
+    const dim3 grid = cast_grid(a.blocks);
     const int64_t bytes = a.blocks * kMxBlock * dtype_bytes(DT);
     if (bytes + a.blocks * mx_block_bytes(FMT) >= kStreamBoth)
         mx_quantize<FMT, DT, 2><<<grid, dim3(kThreads), 0, stream>>>(a);
@@ -1910,7 +1922,7 @@ hipError_t run_quantize(const MxCastArgs &a, hipStream_t stream) {
 
 template <int FMT, int DT>
 hipError_t run_dequantize(const MxCastArgs &a, hipStream_t stream) {
-    const dim3 grid((uint32_t)((a.blocks + kCastBlocks - 1) / kCastBlocks));
+    const dim3 grid = cast_grid(a.blocks);
     if (a.blocks * kMxBlock * dtype_bytes(DT) >= kStreamBytes)
         mx_dequantize<FMT, DT, true><<<grid, dim3(kThreads), 0, stream>>>(a);
     else

@@ -271,3 +271,31 @@ def test_more_columns_than_a_grid_dimension_holds(gpu, xfmt, wfmt, rows, n):
     assert np.array_equal(y[:, where].float().cpu().numpy(), want)
     y[:, where] = 0.0
     assert not y.any()
+
+
+@pytest.mark.parametrize("rows", [2 ** 32 - 1, 2 ** 32 - 256])
+def test_casts_of_as_many_blocks_as_one_call_takes(gpu, rows):
+    """A column of 2^32 - 1 elements is as many blocks.  Zeros but for its ends and the borders
+    of a grid's dimension."""
+    torch = gpu
+    rng = np.random.default_rng(1)
+    at = [0, 255, 256, 2 ** 31 - 1, 2 ** 31, 2 ** 32 - 258, rows - 257, rows - 256, rows - 2,
+          rows - 1]
+    at = sorted(set(at))
+    values = rng.choice([-3.0, -1.0, 0.5, 1.5, 6.0], len(at))
+    x = torch.zeros(rows, 1, dtype=torch.bfloat16, device="cuda")
+    for i, v in zip(at, values):
+        x[i] = v
+    q = zs.Mx.empty(rows, 1, "fp4")
+    zs.zs_mx_quantize(x, q, torch.cuda.current_stream())
+    codes, scales = ref.encode(values[:, None], "fp4")
+    for n, i in enumerate(at):
+        assert np.array_equal(q.codes[i].cpu().numpy(), codes[n])
+        assert q.scales[i].item() == scales[n, 0]
+    x.fill_(7.0)
+    zs.zs_mx_dequantize(q, x, torch.cuda.current_stream())
+    for i, v in zip(at, values):
+        assert x[i].item() == v
+        x[i] = 0.0
+    part = 2 ** 28
+    assert not any(x[i:i + part].any().item() for i in range(0, rows, part))
