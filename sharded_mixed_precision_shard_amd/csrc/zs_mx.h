@@ -56,6 +56,11 @@ struct MxProductArgs {
     uint32_t *counters;           // one per tile, 0 between calls
 };
 
+// Whether 32-bit offsets below 2^31 reach `rows` rows that lie ld bf16 elements apart.  ld may
+// be anything up to 2^59, as that of a single row.
+constexpr int64_t kMxReach = int64_t(1) << 31;
+constexpr bool mx_rows_reach(int64_t ld, int64_t rows) { return ld < kMxReach / (2 * rows); }
+
 constexpr int64_t kMxCounterBytes = 65536;
 constexpr int64_t kMxCounters = kMxCounterBytes / 4;
 constexpr int64_t kMxPartBytes = ZS_MX_WORKSPACE_BYTES - kMxCounterBytes;

@@ -1048,7 +1048,6 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
 
 // A bf16 operand that DMA can take to LDS: rows a multiple of 16 bytes apart, and the
 // rows of a tile (or of a step) inside the reach of a 32-bit offset.
-constexpr int64_t kReach = int64_t(1) << 31;
 
 // y = x w^T.  x goes through LDS by DMA, four steps deep.  w's codes stay packed: a lane
 // loads the block that it multiplies straight into registers, three steps ahead, and
@@ -1770,7 +1769,7 @@ hipError_t run_rows(MxProductArgs a, void *workspace, const MxDevice &dev, hipSt
 // Whether DMA can take the bf16 operand: 16-byte chunks of its rows at 16-byte addresses,
 // `rows` of them within a 32-bit offset.
 bool dma_takes(const MxProductArgs &a, int64_t rows) {
-    return (uintptr_t)a.p % 16 == 0 && a.ldp % 8 == 0 && a.ldp * 2 * rows < kReach;
+    return (uintptr_t)a.p % 16 == 0 && a.ldp % 8 == 0 && mx_rows_reach(a.ldp, rows);
 }
 
 // Rows of x up to which the kernel of few rows is taken: where a tiled kernel takes the
@@ -1960,10 +1959,10 @@ hipError_t launch_mx_product(MxLeft left, int right, MxProductArgs a, void *work
     // what the kernels on whole chunks take
     const bool rows = left == kLeftRows && a.q.nb >= 8 && dma_takes(a, 256);
     const bool fp4 = left == kLeftFp4 && right == kRightFp4 && a.q.nb >= kStep4Blocks &&
-                     a.q.nb * 16 * 256 < kReach;
+                     a.q.nb * 16 * 256 < kMxReach;
     // dy^T's chunks lie along i, where a last one that is not whole could reach past the matrix
     const bool cols = right >= kRightCols && dma_takes(a, 256) &&
-                      (left == kLeftRows || a.I % 8 == 0) && a.q.nb * 32 * kStep < kReach;
+                      (left == kLeftRows || a.I % 8 == 0) && a.q.nb * 32 * kStep < kMxReach;
     if (right < kRightCols && a.I <= (rows || fp4 ? kFewTiled : kFewRows))
         switch (left * 4 + right) {
             case kLeftRows * 4 + kRightFp4:

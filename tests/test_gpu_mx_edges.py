@@ -2,6 +2,8 @@
 codes through every kernel, powers of two at both ends, scales far apart, sums of many
 splits, outputs of few rows or columns.  Inputs and tolerances as in test_gpu_mx_product.py:
 whole numbers times powers of two give equal results, normals stay within C 2^-23 sum|p|."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -299,3 +301,21 @@ def test_casts_of_as_many_blocks_as_one_call_takes(gpu, rows):
         x[i] = 0.0
     part = 2 ** 28
     assert not any(x[i:i + part].any().item() for i in range(0, rows, part))
+
+
+@pytest.mark.parametrize("ld", [2 ** 22, 2 ** 54, 2 ** 55, 3 * 2 ** 54, 2 ** 58])
+def test_one_row_of_any_distance(gpu, workspace, ld):
+    """A single row has no next one, and its distance to that may be any number."""
+    torch = gpu
+    for op, size in (("dgrad", (1, 264, 320)), ("wgrad", (1, 264, 320)), ("linear", (1, 264, 320))):
+        case = Case(torch, op, *size, "fp4", True, 2)
+        _, out = case.out(torch.float32)
+        a = zs.ZsMatrix(case.a.data_ptr(), 1, case.a.shape[1], ld, 0, 0)
+        to = zs._matrix(out, "out")
+        lib, stream = zs.load_library(), torch.cuda.current_stream().cuda_stream
+        args = [ctypes.byref(a), case.b.ref, ctypes.byref(to)]
+        if op == "wgrad":
+            args.append(0)
+        call = lib.zs_mx_linear if op == "linear" else getattr(lib, "zs_mx_linear_" + op)
+        assert call(*args, workspace.data_ptr(), stream) == zs.ZS_OK
+        case.check_equal(out)
