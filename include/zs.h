@@ -608,8 +608,9 @@ typedef struct {
  *
  * The spans of matrix, codes and scales must not overlap (ZS_ERR_ALIASING).
  * zero rows or cols: ZS_OK, nothing enqueued.  At most 2^32 - 1 blocks.  One
- * kernel and nothing else is enqueued, and errors are reported synchronously
- * before that; the arguments are checked before the state of the library.
+ * kernel and nothing else is enqueued on `stream` (a hipStream_t; NULL = the
+ * null stream), and errors are reported synchronously before that; the
+ * arguments are checked before the state of the library.
  */
 int zs_mx_quantize(const zs_matrix *x, const zs_mx *out, void *stream);
 int zs_mx_dequantize(const zs_mx *x, const zs_matrix *out, void *stream);
@@ -625,11 +626,15 @@ int zs_mx_dequantize(const zs_mx *x, const zs_matrix *out, void *stream);
  * y, dx and dw are bf16 or fp32 and written whole (rows ld elements apart: the
  * gaps are left as they were).  A sum over no elements is 0.
  *
- * Numerics: a block's elements are exact in bf16 (see zs_mx_dequantize), so are
- * the products in fp32, and the sums are fp32; each output is rounded once to its
- * type.  The order of a sum is fixed by the sizes, the device and whether there
- * is a workspace: the same call gives the same bits.  Infinities and NaN go
- * where the formula takes them; an element that the layout pads takes no part.
+ * Numerics: a block's elements are taken as bf16, which holds them, so products
+ * are exact in fp32, and the sums are fp32; each output is rounded once to its
+ * type.  Only elements that are no multiple of 2^-133, bf16's smallest denormal
+ * (fp8 blocks of b < 3 may have such), or past its largest number (b > 252 in fp4,
+ * > 246 in fp8, to which no finite input is quantised) are rounded to bf16, the
+ * latter to an infinity; fp4 x fp4 multiplies the codes and powers of two
+ * themselves.  The order of a sum is fixed by the sizes, the device and whether
+ * there is a workspace: the same call gives the same bits.  Infinities and NaN
+ * go where the formula takes them; an element that the layout pads takes no part.
  *
  *   workspace : DEVICE memory of the caller, ZS_MX_WORKSPACE_BYTES, 16-byte
  *               aligned, set to zero once before its first call (each call

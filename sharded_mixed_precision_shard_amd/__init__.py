@@ -1365,7 +1365,7 @@ def _mx_done(rc, name, check) -> int:
 
 def zs_mx_quantize(x, out, stream=None, check=True) -> int:
     """Quantise the matrix x (bf16, fp16 or fp32) into the blocks of ``out``, an Mx
-    of its size."""
+    of its size.  ``stream`` None is the null stream, not torch's current one."""
     m, ref = _matrix(x, "x"), _held(out, "out")
     _mx_ready("zs_mx_quantize", out, x)
     rc = (_lib or load_library()).zs_mx_quantize(ctypes.byref(m), ref, _stream_handle(stream))
@@ -1373,7 +1373,8 @@ def zs_mx_quantize(x, out, stream=None, check=True) -> int:
 
 
 def zs_mx_dequantize(x, out, stream=None, check=True) -> int:
-    """Write the values of an Mx into a matrix of its size (bf16, fp16 or fp32)."""
+    """Write the values of an Mx into a matrix of its size (bf16, fp16 or fp32).
+    ``stream`` None is the null stream."""
     ref, m = _held(x, "x"), _matrix(out, "out")
     _mx_ready("zs_mx_dequantize", x, out)
     rc = (_lib or load_library()).zs_mx_dequantize(ref, ctypes.byref(m), _stream_handle(stream))
@@ -1383,7 +1384,7 @@ def zs_mx_dequantize(x, out, stream=None, check=True) -> int:
 def zs_mx_linear(x, w, y, stream=None, workspace=None, check=True) -> int:
     """y [M, N] = x [M, K] w^T for a bf16 x and an Mx w [N, K]; y is bf16 or fp32.
     With a ``workspace`` (mx_workspace) a product of few output tiles splits its
-    sum over more of the device."""
+    sum over more of the device.  ``stream`` None is the null stream."""
     ref, mx, my = _held(w, "w"), _matrix(x, "x"), _matrix(y, "y")
     space = _mx_ready("zs_mx_linear", w, x, y, workspace)
     rc = (_lib or load_library()).zs_mx_linear(ctypes.byref(mx), ref, ctypes.byref(my), space,
@@ -1392,7 +1393,7 @@ def zs_mx_linear(x, w, y, stream=None, workspace=None, check=True) -> int:
 
 
 def zs_mx_product(x, w, y, stream=None, workspace=None, check=True) -> int:
-    """zs_mx_linear of an x that is an Mx itself."""
+    """zs_mx_linear of an x that is an Mx itself.  ``stream`` None is the null stream."""
     ref, refx, my = _held(w, "w"), _held(x, "x"), _matrix(y, "y")
     space = _mx_ready("zs_mx_product", w, x, y, workspace)
     rc = (_lib or load_library()).zs_mx_product(refx, ref, ctypes.byref(my), space,
@@ -1401,7 +1402,8 @@ def zs_mx_product(x, w, y, stream=None, workspace=None, check=True) -> int:
 
 
 def zs_mx_linear_dgrad(dy, w, dx, stream=None, workspace=None, check=True) -> int:
-    """dx [M, K] = dy [M, N] w for a bf16 dy and an Mx w [N, K]; dx is bf16 or fp32."""
+    """dx [M, K] = dy [M, N] w for a bf16 dy and an Mx w [N, K]; dx is bf16 or fp32.
+    ``stream`` None is the null stream."""
     ref, my, mx = _held(w, "w"), _matrix(dy, "dy"), _matrix(dx, "dx")
     space = _mx_ready("zs_mx_linear_dgrad", w, dy, dx, workspace)
     rc = (_lib or load_library()).zs_mx_linear_dgrad(ctypes.byref(my), ref, ctypes.byref(mx), space,
@@ -1411,7 +1413,8 @@ def zs_mx_linear_dgrad(dy, w, dx, stream=None, workspace=None, check=True) -> in
 
 def zs_mx_linear_wgrad(dy, x, dw, add=False, stream=None, workspace=None, check=True) -> int:
     """dw [N, K] = dy [M, N]^T x for a bf16 dy and the activation x [M, K] kept as an
-    Mx; dw is bf16 (a partial of the step) or fp32, where ``add`` adds to it."""
+    Mx; dw is bf16 (a partial of the step) or fp32, where ``add`` adds to it.
+    ``stream`` None is the null stream."""
     ref, my, mw = _held(x, "x"), _matrix(dy, "dy"), _matrix(dw, "dw")
     space = _mx_ready("zs_mx_linear_wgrad", x, dy, dw, workspace)
     rc = (_lib or load_library()).zs_mx_linear_wgrad(ctypes.byref(my), ref, ctypes.byref(mw),

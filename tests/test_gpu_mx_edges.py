@@ -319,3 +319,41 @@ def test_one_row_of_any_distance(gpu, workspace, ld):
         call = lib.zs_mx_linear if op == "linear" else getattr(lib, "zs_mx_linear_" + op)
         assert call(*args, workspace.data_ptr(), stream) == zs.ZS_OK
         case.check_equal(out)
+
+
+@pytest.mark.parametrize("op", OPS)
+@pytest.mark.parametrize("fmt", ["fp4", "fp8"])
+@pytest.mark.parametrize("rows", [3, 40, 300])
+@pytest.mark.parametrize("byte", [246, 250, 252, 253, 254])
+def test_bytes_past_those_of_finite_inputs(gpu, workspace, op, fmt, rows, byte):
+    """Bytes that no finite bf16 matrix is quantised to: elements past bf16's largest are
+    infinite in a product, but for fp4 x fp4, which takes the codes themselves.  One element of
+    the depth is not zero, and each column of the output has another code there."""
+    torch = gpu
+    case = Case(torch, op, *sized(op, rows, 264, 304), fmt, True, 2, "fp4")
+    case.b.codes.zero_()
+    case.b.scales.fill_(byte)
+    codes = np.arange(264) % (16 if fmt == "fp4" else 256)
+    codes[np.isnan(ref.code_values(fmt)[codes])] = 0
+    column = torch.from_numpy(codes.astype(np.uint8)).cuda()
+    if op in ("linear", "product"):
+        case.b.codes[:, 0] = column
+    elif fmt == "fp4":
+        case.b.codes[0, :132] = column[0::2] | (column[1::2] << 4)
+    else:
+        case.b.codes[0, :264] = column
+    if op == "product":
+        case.a.codes.fill_(0x22)                        # ones, times 2^-40
+        case.a.codes[:, 304 // 2:] = 0
+        case.a.scales.fill_(127 - 40)
+    else:
+        case.a.fill_(2.0 ** -40)
+    values = ref.code_values(fmt)[codes] * 2.0 ** (byte - 127)
+    if not (op == "product" and fmt == "fp4"):
+        past = np.abs(values) > 2.0 ** 128 - 2.0 ** 120          # bf16's largest
+        values = np.where(past, np.copysign(np.inf, values), values)
+    case.want = np.broadcast_to(values * 2.0 ** -40, case.shape)
+    for space in (None, workspace):
+        _, out = case.out(torch.float32)
+        case.call(out, space)
+        assert np.array_equal(out.cpu().numpy(), case.want.astype(np.float32))
