@@ -541,7 +541,7 @@ Request base_request(float *master, void *m, void *v, uint16_t *param, int k, in
 int zs_detail::mx_device(MxDevice *out) {
     int dev = 0;
     const int st = current_device(&dev);
-    if (st == ZS_OK) *out = {g_dev[dev].cus, g_dev[dev].xcds};
+    if (st == ZS_OK) *out = {g_dev[dev].cus};
     return st;
 }
 

@@ -14,7 +14,6 @@ namespace zs_detail {
 // The device the library runs on: zs_api.hip checks that it is prepared.
 struct MxDevice {
     int cus;
-    int xcds;
 };
 int mx_device(MxDevice *out);
 int mx_launched(hipError_t e);  // ZS_OK, or ZS_ERR_DEVICE with the error recorded

@@ -435,7 +435,9 @@ struct HeldStage {
             scale[k] = x.scales[at];
         }
     }
-    // Numbers of no consequence go to LDS where `in` is false (the other operand's are 0).
+    // Where `in` is false the numbers go to LDS times 2^-127.  A bf16 operand's are 0 there, and
+    // two stored operands' products, below 2^-235, are 0 in fp32 (a NaN among them is one of the
+    // row's, which the row's sum has all the same).
     __device__ __forceinline__ void store(char *lds, int tid, bool in = true) {
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
@@ -626,7 +628,9 @@ __device__ __forceinline__ void finish_tile(const MxProductArgs &a,
     // Splits are joined two by two: of splits [s, s + n) and [s + n, s + 2 n) the one that is
     // done first leaves its sums and ends, the other adds them to its own and goes on with
     // both.  The tree is the same every time and an addition's two sides may change places,
-    // so the order in which splits end does not show.
+    // so the order in which splits end does not show.  (Tiles of 256 x 256 are never split, see
+    // plan; left out of them, this made the compiler issue the fp4 kernel's transfers in another
+    // order, 70B product 1062 us instead of 1034.)
     const uint32_t here = (uint32_t)wave * (FJ * FI * 1024) + (uint32_t)lane * 4;
     const uint32_t slots = (uint32_t)tile * (uint32_t)a.splits;
     for (int n = 1; n < a.splits; n *= 2) {
@@ -903,13 +907,14 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
     constexpr int FI = BI / WI / 32, FJ = BJ / WJ / 32;
     constexpr int P_BYTES = BI * 128, Q_BYTES = BJ * 128;
     constexpr int EACH_P = BI * 8 / NT, EACH_Q = BJ * 8 / NT;
-    // two stages, each an array of its own: the compiler sees that what is read of one
-    // does not wait for what is on its way into the other
+    // two stages, each an array of its own: the compiler sees that the codes read of one do not
+    // wait for what is on its way into the other (the reads of scales do: it cannot tell them
+    // from what the transfers write)
     __shared__ __attribute__((aligned(128))) char all0[KG][P_BYTES + Q_BYTES];
     __shared__ __attribute__((aligned(128))) char all1[KG][P_BYTES + Q_BYTES];
-    constexpr int SC = (BI + BJ + NT - 1) / NT;  // rows whose scales a thread takes
-    __shared__ uint64_t all_scales0[KG][SC * NT];
-    __shared__ uint64_t all_scales1[KG][SC * NT];
+    static_assert(BI + BJ <= NT, "a thread takes the scales of one row at most");
+    __shared__ uint64_t all_scales0[KG][NT];
+    __shared__ uint64_t all_scales1[KG][NT];
 
     const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / NT);
     const int tid = threadIdx.x % NT, lane = tid % kWave;
@@ -933,13 +938,8 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
     // a wave's chunk k: eight rows, lane / 8 the row, lane % 8 the place in it
     const int row = wave * 8 + lane / 8, chunk = (lane % 8) ^ (row >> 1 & 7);
     const uint32_t p_off = (uint32_t)row * row_bytes + (uint32_t)chunk * 16u;
-    const uint8_t *my_scales[SC];
-#pragma unroll
-    for (int c = 0; c < SC; ++c) {
-        const int at = c * NT + tid;
-        my_scales[c] = at < BI ? a.px.scales + (int64_t)min(i0 + at, a.I - 1) * nb
-                               : a.q.scales + (int64_t)min(j0 + at - BI, a.J - 1) * nb;
-    }
+    const uint8_t *my_scales = tid < BI ? a.px.scales + (int64_t)min(i0 + tid, a.I - 1) * nb
+                                        : a.q.scales + (int64_t)min(j0 + tid - BI, a.J - 1) * nb;
 
     // tiles begin at different steps: the rows of wide operands lie a power of two apart, and
     // workgroups that read the same columns at a time would meet on few of the L2's channels
@@ -962,19 +962,10 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
             dma16(q_buf, lds + P_BYTES + (k * (NT / 8) + wave * 8) * 128,
                   off + (uint32_t)(k * (NT / 8)) * row_bytes);
     };
-    struct Scales {
-        Scales8 of[SC];
-    };
     auto fetch_scales = [&](int step) {
-        Scales s;
-#pragma unroll
-        for (int c = 0; c < SC; ++c)
-            s.of[c].load(my_scales[c], block_of(step), nb);
+        Scales8 s;
+        s.load(my_scales, block_of(step), nb);
         return s;
-    };
-    auto put_scales = [&](uint64_t *to, const Scales &s) {
-#pragma unroll
-        for (int c = 0; c < SC; ++c) to[c * NT + tid] = s.of[c].value();
     };
 
     f32x16 acc[FJ][FI];
@@ -1015,23 +1006,23 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_fp4(MxProductArg
 
     if (steps > 0) {
         fetch(lds0, 0);
-        put_scales(scales0, fetch_scales(0));
+        scales0[tid] = fetch_scales(0).value();
     }
     // two steps a turn: a split ends with a whole turn, or with the row, past which all is 0
 #pragma unroll 1
     for (int step = 0; step < steps; step += 2) {
         stage_ready<0>();
         fetch(lds1, step + 1);
-        Scales s = fetch_scales(step + 1);
+        Scales8 s = fetch_scales(step + 1);
         __builtin_amdgcn_sched_barrier(0);
         multiply(lds0, scales0);
-        put_scales(scales1, s);
+        scales1[tid] = s.value();
         stage_ready<0>();
         fetch(lds0, step + 2);
         s = fetch_scales(step + 2);
         __builtin_amdgcn_sched_barrier(0);
         multiply(lds1, scales1);
-        put_scales(scales0, s);
+        scales0[tid] = s.value();
     }
     stage_ready<0>();
     constexpr int HALF = WI * WJ / 2, SCRATCH = (P_BYTES + Q_BYTES) / HALF;
