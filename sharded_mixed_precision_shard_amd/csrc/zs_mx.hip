@@ -1250,7 +1250,8 @@ __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_rows(MxProductAr
 // dgrad, 8192 x 4096 of depth 11008 0.58 ms (1.27 PFLOP/s, the matrix pipe busy 66 % of the time,
 // LDS 42 %); wgrad, 4096 x 11008 of depth 8192 in fp8 0.68 (1.08; 55-59 % and 37 %).  LDS carries
 // both operands and their writes here, and is what bounds the small tiles: 64 x 64 takes three
-// times as long per product.
+// times as long per product.  The compiler computes the size of a block's buffer in a vector
+// register and wraps each of its loads in a loop over lanes, of one turn.
 template <int BI, int BJ, int WI, int WJ, int KG, bool PC, bool F8>
 __global__ __launch_bounds__(WI *WJ *KG *kWave, 2) void mx_tile_cols(MxProductArgs a) {
     constexpr int NT = WI * WJ * kWave;
@@ -1709,6 +1710,8 @@ void plan(MxProductArgs *a, int bi, int bj, int groups, int depth, int turn, int
 // with the next smaller or larger choice).  Tiles of 256 x 256 from a tile per compute unit
 // on: bf16 by fp4, K = 4096, 4096 x 4096 107 against 138 in tiles of 128, 2048 x 4096 81 and 71;
 // dgrad 111 and 137, 91 and 72; fp4 48 and 60, 38 and 33; any strides 130 and 167, 115 and 89.
+// The elements alone count, though an output of few rows or columns leaves part of such a tile
+// empty: 64 rows, N = 262144 340, N = 261888 (in tiles of 64 x 128) 212.
 constexpr int64_t kTile256 = 256 * 256;
 // Tiles of 128 x 128, more than a compute unit each, in one wave group; up to that many in two,
 // since a wave per SIMD hides little: dgrad 2048 x 4096 (512 tiles) 72 in one, 79 in two groups,
@@ -1766,7 +1769,10 @@ bool dma_takes(const MxProductArgs &a, int64_t rows) {
 // Rows of x up to which the kernel of few rows is taken: where a tiled kernel takes the
 // operands, too, it is faster from there on (K = 8192, N = 28672, bf16 x: 8 rows 38 us here and 46
 // in tiles of 32, 16 rows 42 and 47, 32 rows 129 and 48; fp4 x: 16 rows 35 and 40, 32 rows 50
-// and 41).
+// and 41).  Where only the tiles through registers take them the border that suits depends on the
+// size of w, and 64 suits small ones (64 rows here and in those tiles: bf16 x at odd strides,
+// N = 1003, K = 2001 12.4 and 12.6, N = 4096, K = 4096 52 and 16, N = 28672, K = 8192 414 and 101; fp8
+// x, the latter two 12.6 and 15.9, 149 and 91).
 constexpr int kFewRows = 64, kFewTiled = 16;
 
 template <int LEFT, bool F8, int MF, int NF, int WAVES>
@@ -1791,7 +1797,8 @@ hipError_t run_few(MxProductArgs a, void *workspace, const MxDevice &dev, hipStr
 
 // Strips of 64 columns read x a quarter as often as strips of 16, and leave a quarter of the
 // workgroups: bf16 x, K = 8192, N = 28672, 16 rows 42 us against 72, one row 36 and 38; K = 4096,
-// N = 11008, 16 rows 11.2 and 16.4, one row 10.3 and 9.2; N = 4096, 10.9 and 6.8.  An x in blocks
+// N = 11008, 16 rows 11.2 and 16.4, one row 10.3 and 9.2; N = 4096, 10.9 and 6.8.  With fp8 w, in
+// the same order, 67 and 84, 63 and 60; 14.9 and 19.7, 14.0 and 13.8; 14.7 and 8.5.  An x in blocks
 // is short: strips of 16 are as fast or faster, up to the 2^23 of 512 threads each that are more
 // than a grid's dimension holds.
 constexpr int64_t kMostStrips = (int64_t(1) << 23) - 1;
