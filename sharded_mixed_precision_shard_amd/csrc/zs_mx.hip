@@ -1771,8 +1771,8 @@ bool dma_takes(const MxProductArgs &a, int64_t rows) {
 // in tiles of 32, 16 rows 42 and 47, 32 rows 129 and 48; fp4 x: 16 rows 35 and 40, 32 rows 50
 // and 41).  Where only the tiles through registers take them the border that suits depends on the
 // size of w, and 64 suits small ones (64 rows here and in those tiles: bf16 x at odd strides,
-// N = 1003, K = 2001 12.4 and 12.6, N = 4096, K = 4096 52 and 16, N = 28672, K = 8192 414 and 101; fp8
-// x, the latter two 12.6 and 15.9, 149 and 91).
+// N = 1003, K = 2001 12.4 and 12.6, N = 4096, K = 4096 52 and 16, N = 28672, K = 8192 414 and 101;
+// fp8 x, the latter two 12.6 and 15.9, 149 and 91).
 constexpr int kFewRows = 64, kFewTiled = 16;
 
 template <int LEFT, bool F8, int MF, int NF, int WAVES>

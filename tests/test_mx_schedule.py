@@ -5,7 +5,8 @@ mx_tile_rows waits by count: a step may begin when at most N operations are stil
 their way, and they end in the order in which they were issued.  That is a wait for the
 step's transfers to LDS only if N others were issued after them: the transfers of the
 first three steps come before the loads of their codes, and nothing is moved to the
-other side of a branch."""
+other side of a branch.  mx_tile_cols waits for all but a block's loads, which have to
+follow each step's transfers."""
 import os
 import re
 import shutil
@@ -17,6 +18,7 @@ import pytest
 import sharded_mixed_precision_shard_amd as zs
 
 TOOL = shutil.which("llvm-objdump") or "/opt/rocm/llvm/bin/llvm-objdump"
+COLS = re.compile(r"mx_tile_colsILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELb[01]ELb([01])E")
 ROWS = re.compile(r"mx_tile_rowsILi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELi(\d+)ELb([01])E")
 
 
@@ -84,3 +86,25 @@ def test_the_first_step_waits_for_its_transfers():
         waits = [n for n, e in enumerate(seq) if isinstance(e, int)]
         behind = [e for e in seq[each:waits[-1]] if e in ("D", "c", "o")]
         assert seq[waits[-1]] <= len(behind), match.group(0)
+
+
+@pytest.mark.skipif(not os.path.exists(TOOL), reason="no llvm-objdump")
+def test_a_block_s_loads_follow_each_step_s_transfers():
+    found = kernels(COLS)
+    assert len(found) == 16
+    for match, lines in found.items():
+        bi, _, wi, wj, _, f8 = (int(x) for x in match.groups())
+        each, loads = bi * 8 // (wi * wj * 64), 3 if f8 else 2
+        seq = events(lines)
+        at = [n for n, e in enumerate(seq) if e == "D"]
+        # before the loop, and the two steps of a turn
+        assert len(at) == 3 * each, match.group(0)
+        for stage in range(3):
+            last = at[(stage + 1) * each - 1]
+            end = at[(stage + 1) * each] if stage < 2 else \
+                next(n for n in range(last, len(seq)) if seq[n] == 0)
+            behind = [e for e in seq[last:end] if e in ("c", "o")]
+            assert len(behind) >= loads, match.group(0)
+        waits = [seq[n] for n in range(at[0], at[-1]) if isinstance(seq[n], int)
+                 and "|" in seq[n + 1:n + 2]]
+        assert waits == [loads, loads], match.group(0)
